@@ -8,14 +8,17 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libgnsilu.so")
-SOURCES = [os.path.join(CSRC, "gn_api.hip")]
-DEPENDS = SOURCES + [os.path.join(CSRC, "gn_kernels.hpp"), os.path.join(INCLUDE, "gnsilu.h")]
+SOURCES = [os.path.join(CSRC, f) for f in ("gn_api.hip", "gn_backward.hip", "gn_layer_norm.hip")]
+DEPENDS = SOURCES + [os.path.join(CSRC, f) for f in ("gn_conv.hpp", "gn_host.hpp", "gn_kernels.hpp",
+                                                     "gn_rows.hpp", "gn_types.hpp")]
+DEPENDS.append(os.path.join(INCLUDE, "gnsilu.h"))
 ARCH = "gfx950"
 
 
@@ -26,15 +29,19 @@ def hipcc() -> str:
     raise RuntimeError("hipcc not found; set HIPCC or install ROCm")
 
 
-def compile_command(out: str):
+def compile_command(source: str, out: str):
     return [
-        hipcc(), "--offload-arch=" + ARCH, "-O3", "-std=c++17", "-fPIC", "-shared",
+        hipcc(), "--offload-arch=" + ARCH, "-O3", "-std=c++17", "-fPIC", "-c",
         # no packed fp32 (v_pk_*_f32) instructions anywhere in device code
         "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
         "-Wall", "-Wno-unused-command-line-argument",
         "-I", INCLUDE, "-I", CSRC,
-        "-o", out, *SOURCES,
+        "-o", out, source,
     ]
+
+
+def link_command(objects, out: str):
+    return [hipcc(), "--offload-arch=" + ARCH, "-fPIC", "-shared", "-o", out, *objects]
 
 
 def sanitizer_command(out: str):
@@ -79,17 +86,30 @@ def build_host_sanitized(out: str, verbose: bool = False) -> str:
     return out
 
 
+def _run(cmds, verbose, what):
+    """Runs the commands at once; their stderr, or RuntimeError if one fails."""
+    procs = []
+    for cmd in cmds:
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        procs.append(subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.PIPE,
+                                      text=True))
+    outs = [p.communicate() for p in procs]
+    if any(p.returncode != 0 for p in procs):
+        sys.stderr.write("".join(o + e for o, e in outs))
+        raise RuntimeError("hipcc failed %s" % what)
+    return "".join(e for _, e in outs)
+
+
 def build(verbose: bool = False) -> str:
-    tmp = LIB + ".tmp"
-    cmd = compile_command(tmp)
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        sys.stderr.write(res.stdout + res.stderr)
-        raise RuntimeError("hipcc failed building libgnsilu.so")
+    with tempfile.TemporaryDirectory(prefix="gnsilu_build_") as tmpdir:
+        objects = [os.path.join(tmpdir, os.path.basename(f) + ".o") for f in SOURCES]
+        noise = _run([compile_command(f, o) for f, o in zip(SOURCES, objects)], verbose,
+                     "building libgnsilu.so")
+        tmp = LIB + ".tmp"
+        noise += _run([link_command(objects, tmp)], verbose, "linking libgnsilu.so")
     # hipcc's host pass does not know the packed-fp32 feature; drop that note.
-    noise = [ln for ln in res.stderr.splitlines()
+    noise = [ln for ln in noise.splitlines()
              if ln.strip() and "packed-fp32-ops" not in ln and "is not a recognized feature" not in ln]
     if verbose and noise:
         sys.stderr.write("\n".join(noise) + "\n")

@@ -22,14 +22,24 @@ channels-last (4-D / 5-D) / not contiguous rows, weight/bias not fp32, bf16 or
 fp16 (both of one type) on the same device.  Arguments no GroupNorm accepts raise ValueError; a failed HIP
 call raises RuntimeError.
 
+For training: layer_norm_rows and layer_norm_rows_backward,
+group_norm_silu_rows_backward (after group_stats_rows and apply_rows), and
+8-bit checkpoints of the input that both backward passes take in its place
+(checkpoint_rows, restore_rows, the ``checkpoint`` argument of layer_norm_rows
+and apply_rows).  Like the rest they run with autograd disabled, i.e. inside a
+torch.autograd.Function.
+
 The raw C entry points are re-exported under their C names (gn_silu_nhwc,
 gn_silu_rows, gn_silu_nhwc_strided, gn_silu_ndhwc, gn_stats_rows,
 gn_apply_rows, gn_profile_rows, gn_plan_rows, their *_dtype forms,
-gn_silu_rows_noalloc, gn_kernel_name, gn_status_string, gn_version,
+gn_silu_rows_noalloc, gn_layer_norm_rows and gn_layer_norm_rows_backward,
+gn_silu_rows_backward, gn_apply_rows_save, gn_checkpoint_rows,
+gn_restore_rows, gn_kernel_name, gn_status_string, gn_version,
 gn_device_info).
 """
 import ctypes
 import enum
+import math
 import os
 
 # torch first: its wheel bundles a HIP runtime (torch/lib/libamdhip64.so,
@@ -107,6 +117,18 @@ lib.gn_apply_rows_dtype.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i
 lib.gn_profile_rows_dtype.argtypes = [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _f32, _int,
                                       _int, _vp, _int, ctypes.POINTER(_f32),
                                       ctypes.POINTER(_int)]
+lib.gn_checkpoint_rows.argtypes = [_vp, _i64, _vp, _vp, _i64, _i64, _int, _vp]
+lib.gn_restore_rows.argtypes = [_vp, _vp, _vp, _i64, _i64, _i64, _int, _vp]
+lib.gn_layer_norm_rows.argtypes = [_vp, _i64, _vp, _vp, _vp, _i64, _i64, _i64, _f32, _int, _vp,
+                                   _vp, _vp, _vp, _vp]
+lib.gn_layer_norm_rows_backward_workspace.argtypes = [_i64, _i64, _int, _i64p]
+lib.gn_layer_norm_rows_backward.argtypes = [_vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp,
+                                            _i64, _vp, _vp, _i64, _i64, _int, _vp, _i64, _vp]
+lib.gn_apply_rows_save.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64,
+                                   _int, _int, _vp]
+lib.gn_silu_rows_backward_workspace.argtypes = [_i64, _i64, _i64, _i64, _int, _i64p]
+lib.gn_silu_rows_backward.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64,
+                                      _i64, _i64, _i64, _int, _int, _vp, _i64, _vp]
 lib.gn_plan_rows_dtype.argtypes = [_i64, _i64, _i64, _i64, _int, _i64p]
 lib.gn_plan_single_launch.argtypes = [_i64, _i64, _i64, _i64, _int, _i64p]
 for _name in ("gn_silu_nhwc", "gn_silu_rows", "gn_silu_nhwc_strided", "gn_stats_rows",
@@ -115,7 +137,10 @@ for _name in ("gn_silu_nhwc", "gn_silu_rows", "gn_silu_nhwc_strided", "gn_stats_
               "gn_profile_rows_dtype", "gn_plan_rows_dtype", "gn_silu_ndhwc",
               "gn_silu_ndhwc_dtype", "gn_silu_ndhwc_strided_dtype", "gn_conv3x3_nhwc",
               "gn_conv3x3_plan", "gn_conv3x3_pack_weights", "gn_conv3x3_nhwc_packed",
-              "gn_silu_rows_noalloc", "gn_plan_single_launch", "gn_noalloc_scratch"):
+              "gn_silu_rows_noalloc", "gn_plan_single_launch", "gn_noalloc_scratch",
+              "gn_checkpoint_rows", "gn_restore_rows", "gn_layer_norm_rows",
+              "gn_layer_norm_rows_backward_workspace", "gn_layer_norm_rows_backward",
+              "gn_apply_rows_save", "gn_silu_rows_backward_workspace", "gn_silu_rows_backward"):
     getattr(lib, _name).restype = _int
 lib.gn_plan_rows.argtypes = [_i64, _i64, _i64, _i64, _i64p]
 lib.gn_plan_rows.restype = _int
@@ -154,12 +179,22 @@ gn_apply_rows_dtype = lib.gn_apply_rows_dtype
 gn_profile_rows_dtype = lib.gn_profile_rows_dtype
 gn_plan_rows_dtype = lib.gn_plan_rows_dtype
 gn_plan_single_launch = lib.gn_plan_single_launch
+gn_checkpoint_rows = lib.gn_checkpoint_rows
+gn_restore_rows = lib.gn_restore_rows
+gn_layer_norm_rows = lib.gn_layer_norm_rows
+gn_layer_norm_rows_backward_workspace = lib.gn_layer_norm_rows_backward_workspace
+gn_layer_norm_rows_backward = lib.gn_layer_norm_rows_backward
+gn_apply_rows_save = lib.gn_apply_rows_save
+gn_silu_rows_backward_workspace = lib.gn_silu_rows_backward_workspace
+gn_silu_rows_backward = lib.gn_silu_rows_backward
 gn_status_string = lib.gn_status_string
 gn_version = lib.gn_version
 gn_device_info = lib.gn_device_info
 
 MAX_CHANNELS = 8192
 NOALLOC_SCRATCH_BYTES = 1 << 20   # GN_NOALLOC_SCRATCH_BYTES
+LAYER_NORM_MAX_CHANNELS = 16384   # GN_LAYER_NORM_MAX_CHANNELS
+CHECKPOINT_BLOCK = 32             # GN_CHECKPOINT_BLOCK
 
 
 class GnDtype(enum.IntEnum):
@@ -213,8 +248,15 @@ def _torch():
     return torch
 
 
+# Handle of the current stream of a device, as an integer; without the Stream
+# object that torch.cuda.current_stream builds (0.2 us a call instead of 2.2).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream_handle(t):
     torch = _torch()
+    if _raw_stream is not None:
+        return ctypes.c_void_p(_raw_stream(t.device.index))
     return ctypes.c_void_p(torch.cuda.current_stream(t.device).cuda_stream)
 
 
@@ -350,17 +392,350 @@ def group_stats_rows(x, num_groups, eps=1e-6):
     return r
 
 
-def apply_rows(x, mean, rstd, weight=None, bias=None, apply_silu=True, out=None):
-    """Step three alone on contiguous (N, L, C) rows, given per-(n, g) mean/rstd."""
+def apply_rows(x, mean, rstd, weight=None, bias=None, apply_silu=True, out=None, *,
+               checkpoint=False):
+    """Step three alone on contiguous (N, L, C) rows, given per-(n, g) mean/rstd.
+
+    checkpoint: also return x's 8-bit checkpoint, written in the same pass
+    ((y, Checkpoint8) instead of y; any C up to MAX_CHANNELS), for
+    ``group_norm_silu_rows_backward``."""
     torch = _torch()
     N, L, C = x.shape
     G = mean.shape[-1]
+    if checkpoint:
+        return _apply_rows_save(x, mean, rstd, weight, bias, apply_silu, out, N, L, C, G)
     if out is None:
         out = torch.empty_like(x)
     code = lib.gn_apply_rows_dtype(_ptr(x), _ptr(mean), _ptr(rstd), _ptr(weight), _ptr(bias),
                                    _ptr(out), N, L, C, G, 1 if apply_silu else 0,
                                    _dtype_arg(x) | _affine_arg(weight, bias), _stream_handle(x))
     return _result(code, out)
+
+
+class Checkpoint8:
+    """Rows kept in 8 bits for a backward pass (the format in gnsilu.h):
+    ``codes`` int8 (..., C), ``scales`` uint8 (..., ceil(C / 32)), both
+    contiguous, and the ``dtype`` of the rows that they stand for."""
+
+    def __init__(self, codes, scales, dtype):
+        torch = _torch()
+        if codes.dtype != torch.int8 or scales.dtype != torch.uint8:
+            raise TypeError("a checkpoint holds int8 codes and uint8 scales")
+        if codes.dim() < 1 or tuple(scales.shape) != _scales_shape(codes.shape):
+            raise ValueError("scales must have shape (..., ceil(C / %d))" % CHECKPOINT_BLOCK)
+        if dtype_code(dtype) is None:
+            raise TypeError("unsupported dtype %s" % dtype)
+        if codes.device != scales.device:
+            raise ValueError("codes and scales must be on one device")
+        if not codes.is_contiguous() or not scales.is_contiguous():
+            raise ValueError("codes and scales must be contiguous")
+        self.codes, self.scales, self.dtype = codes, scales, dtype
+
+    shape = property(lambda self: self.codes.shape)
+    device = property(lambda self: self.codes.device)
+
+
+def _scales_shape(shape):
+    return tuple(shape[:-1]) + ((shape[-1] + CHECKPOINT_BLOCK - 1) // CHECKPOINT_BLOCK,)
+
+
+def _empty_checkpoint(shape, device, dtype):
+    torch = _torch()
+    return Checkpoint8(torch.empty(tuple(shape), dtype=torch.int8, device=device),
+                       torch.empty(_scales_shape(shape), dtype=torch.uint8, device=device), dtype)
+
+
+def _row_stride(x):
+    """Elements from one row's start to the next one's for the rows x[..., :],
+    or None when they are not evenly spaced or not dense within a row."""
+    shape, stride = x.shape, x.stride()
+    if x.is_contiguous():
+        return shape[-1]
+    if shape[-1] > 1 and stride[-1] != 1:
+        return None
+    step = None
+    span = 1      # rows covered by the dimensions seen so far
+    for d in range(len(shape) - 2, -1, -1):
+        if shape[d] == 1:
+            continue
+        if step is None:
+            step = stride[d]
+        elif stride[d] != span * step:
+            return None
+        span *= shape[d]
+    return shape[-1] if step is None else step
+
+
+def _rows_of(x):
+    C = x.shape[-1]
+    if C:
+        return x.numel() // C
+    return math.prod(x.shape[:-1])
+
+
+def _dense_like(x):
+    """An uninitialised contiguous tensor of x's shape and type."""
+    torch = _torch()
+    return torch.empty_like(x, memory_format=torch.contiguous_format)
+
+
+def _addr(t):
+    """A tensor's address for a void pointer argument, None for none."""
+    return None if t is None else t.data_ptr()
+
+
+def _gpu_rows(x, name="x"):
+    """Whether x is rows that the library takes: a GPU tensor, no autograd, a
+    supported dtype (raises TypeError for what is no tensor)."""
+    torch = _torch()
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if x.dim() < 1:
+        raise ValueError("%s must have at least one dimension" % name)
+    return (x.device.type == "cuda" and torch.version.hip is not None
+            and not torch.is_grad_enabled() and dtype_code(x.dtype) is not None)
+
+
+def _check_out(out, x):
+    if out.shape != x.shape or out.dtype != x.dtype or out.device != x.device:
+        raise ValueError("out must match in shape, dtype and device")
+
+
+def _stat(t, n, name, x):
+    """A statistics tensor: n contiguous fp32 values on x's device."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a tensor" % name)
+    if t.numel() != n or t.dtype != torch.float32:
+        raise ValueError("%s must hold %d fp32 values" % (name, n))
+    return t.device == x.device and t.is_contiguous()
+
+
+def checkpoint_rows(x):
+    """The 8-bit checkpoint of the rows x[..., :] (a Checkpoint8), or None
+    when the library declines x."""
+    if not _gpu_rows(x):
+        return None
+    step = _row_stride(x)
+    if step is None or x.shape[-1] == 0:
+        return None
+    ck = _empty_checkpoint(x.shape, x.device, x.dtype)
+    code = lib.gn_checkpoint_rows(_addr(x), step, _addr(ck.codes), _addr(ck.scales), _rows_of(x),
+                                  x.shape[-1], dtype_code(x.dtype), _stream_handle(x))
+    return _result(code, ck) if x.numel() else ck
+
+
+def restore_rows(checkpoint, dtype=None, out=None):
+    """The rows that a Checkpoint8 stands for, in ``dtype`` (by default the
+    type they were saved from)."""
+    torch = _torch()
+    if not isinstance(checkpoint, Checkpoint8):
+        raise TypeError("restore_rows takes a Checkpoint8")
+    codes = checkpoint.codes
+    if codes.device.type != "cuda" or torch.is_grad_enabled() or codes.shape[-1] == 0:
+        return None
+    if out is None:
+        dtype = checkpoint.dtype if dtype is None else dtype
+        if dtype_code(dtype) is None:
+            raise TypeError("unsupported dtype %s" % dtype)
+        out = torch.empty(codes.shape, dtype=dtype, device=codes.device)
+    elif (out.shape != codes.shape or out.device != codes.device
+          or dtype_code(out.dtype) is None or (dtype is not None and out.dtype != dtype)):
+        raise ValueError("out must match in shape, dtype and device")
+    step = _row_stride(out)
+    if step is None:
+        return None
+    if not out.numel():
+        return out
+    code = lib.gn_restore_rows(_addr(codes), _addr(checkpoint.scales), _addr(out), step,
+                               _rows_of(codes), codes.shape[-1], dtype_code(out.dtype),
+                               _stream_handle(codes))
+    return _result(code, out)
+
+
+def layer_norm_rows(x, weight=None, bias=None, eps=1e-6, *, stats=False, checkpoint=False,
+                    out=None):
+    """Layer norm of the rows x[..., :] over their C values.
+
+    x: bf16, fp16 or fp32; rows evenly spaced (a slice of wider rows will do),
+    C <= LAYER_NORM_MAX_CHANNELS.  weight, bias: C values each in fp32, bf16 or
+    fp16 (both of one type), or None.  Returns y; with ``stats`` (y, mean,
+    rstd), fp32 of shape x.shape[:-1]; with ``checkpoint`` (y, mean, rstd,
+    Checkpoint8 of x), all written in one pass.  None when the library
+    declines the input (the caller falls back)."""
+    torch = _torch()
+    if not _gpu_rows(x):
+        return None
+    C = x.shape[-1]
+    if not _affine_ok(weight, C, x.device, "weight") or not _affine_ok(bias, C, x.device, "bias"):
+        return None
+    affine = _affine_flag(weight, bias)
+    step = _row_stride(x)
+    if affine is None or step is None or C == 0 or C > LAYER_NORM_MAX_CHANNELS:
+        return None
+    if out is None:
+        out = _dense_like(x)
+        ostep = C
+    else:
+        _check_out(out, x)
+        ostep = _row_stride(out)
+        if ostep is None:
+            return None
+    mean = rstd = ck = None
+    if stats or checkpoint:
+        mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+        rstd = torch.empty_like(mean)
+    if checkpoint:
+        ck = _empty_checkpoint(x.shape, x.device, x.dtype)
+    r = (out, mean, rstd, ck) if checkpoint else (out, mean, rstd) if stats else out
+    if not x.numel():
+        return r
+    code = lib.gn_layer_norm_rows(
+        _addr(x), step, _addr(weight), _addr(bias), _addr(out), ostep, _rows_of(x), C, float(eps),
+        dtype_code(x.dtype) | affine, _addr(mean), _addr(rstd), _addr(ck.codes if ck else None),
+        _addr(ck.scales if ck else None), _stream_handle(x))
+    return _result(code, r)
+
+
+def _saved_input(x, dy):
+    """(ok, x's pointer, codes' and scales' pointers) of a backward pass's
+    input: a tensor like dy or a Checkpoint8 of dy's shape."""
+    if isinstance(x, Checkpoint8):
+        if x.shape != dy.shape:
+            raise ValueError("the checkpoint must have dy's shape")
+        if x.device != dy.device:
+            return False, None, None, None
+        return True, None, _addr(x.codes), _addr(x.scales)
+    if not isinstance(x, _torch().Tensor):
+        raise TypeError("x must be a torch.Tensor or a Checkpoint8")
+    if x.shape != dy.shape:
+        raise ValueError("x must have dy's shape")
+    return x.dtype == dy.dtype and x.device == dy.device, _addr(x), None, None
+
+
+def _weight_gradients(weight, C, dy, wanted):
+    if not wanted:
+        return None, None
+    torch = _torch()
+    dt = torch.float32 if weight is None else weight.dtype
+    return (torch.empty(C, dtype=dt, device=dy.device), torch.empty(C, dtype=dt, device=dy.device))
+
+
+def layer_norm_rows_backward(dy, x, mean, rstd, weight=None, *, weight_grad=True, out=None):
+    """Backward pass of ``layer_norm_rows``: (dx, dweight, dbias).
+
+    x: the forward pass's input, or its Checkpoint8; mean, rstd: as the
+    forward pass returned them.  dweight and dbias have weight's type (fp32
+    without a weight), and are None unless ``weight_grad``.  None when the
+    library declines the input."""
+    torch = _torch()
+    if not _gpu_rows(dy, "dy"):
+        return None
+    C, M = dy.shape[-1], _rows_of(dy)
+    ok, xp, codes, scales = _saved_input(x, dy)
+    ok = _stat(mean, M, "mean", dy) and ok
+    ok = _stat(rstd, M, "rstd", dy) and ok
+    ok = _affine_ok(weight, C, dy.device, "weight") and ok
+    if not ok or C == 0 or C > LAYER_NORM_MAX_CHANNELS:
+        return None
+    step = _row_stride(dy)
+    xstep = C if xp is None else _row_stride(x)
+    if step is None or xstep is None:
+        return None
+    if out is None:
+        out = _dense_like(dy)
+        ostep = C
+    else:
+        _check_out(out, dy)
+        ostep = _row_stride(out)
+        if ostep is None:
+            return None
+    dw, db = _weight_gradients(weight, C, dy, weight_grad)
+    if M == 0:
+        if weight_grad:
+            dw.zero_()
+            db.zero_()
+        return out, dw, db
+    dtype = dtype_code(dy.dtype) | _affine_flag(weight, None)
+    ws, size = None, 0
+    if weight_grad:
+        need = _i64(0)
+        _result(lib.gn_layer_norm_rows_backward_workspace(M, C, dtype, ctypes.byref(need)), None)
+        size = need.value
+        ws = torch.empty(size, dtype=torch.uint8, device=dy.device)
+    code = lib.gn_layer_norm_rows_backward(
+        _addr(dy), step, xp, xstep, codes, scales, _addr(mean), _addr(rstd), _addr(weight), _addr(out),
+        ostep, _addr(dw), _addr(db), M, C, dtype, _addr(ws), size, _stream_handle(dy))
+    return _result(code, (out, dw, db))
+
+
+def _apply_rows_save(x, mean, rstd, weight, bias, apply_silu, out, N, L, C, G):
+    torch = _torch()
+    if out is None:
+        out = _dense_like(x)
+    ck = _empty_checkpoint(x.shape, x.device, x.dtype)
+    code = lib.gn_apply_rows_save(
+        _addr(x), _addr(mean), _addr(rstd), _addr(weight), _addr(bias), _addr(out), _addr(ck.codes),
+        _addr(ck.scales), N, L, C, G, 1 if apply_silu else 0,
+        _dtype_arg(x) | _affine_arg(weight, bias), _stream_handle(x))
+    return _result(code, (out, ck))
+
+
+def group_norm_silu_rows_backward(dy, x, mean, rstd, weight=None, bias=None, apply_silu=True, *,
+                                  weight_grad=True, out=None):
+    """Backward pass of GroupNorm(+SiLU) over contiguous (N, L, C) rows:
+    (dx, dweight, dbias).
+
+    x: the forward pass's input, or its Checkpoint8 (``apply_rows`` with
+    ``checkpoint``); mean, rstd: (N, G) as ``group_stats_rows`` returned them;
+    weight, bias: as in the forward pass.  dweight and dbias have the
+    parameters' type (fp32 without any), and are None unless ``weight_grad``.
+    None when the library declines the input."""
+    torch = _torch()
+    if not _gpu_rows(dy, "dy"):
+        return None
+    if dy.dim() != 3:
+        raise ValueError("group_norm_silu_rows_backward expects (N, L, C) rows, got %d-D"
+                         % dy.dim())
+    N, L, C = dy.shape
+    ok, xp, codes, scales = _saved_input(x, dy)
+    if not isinstance(mean, torch.Tensor) or mean.dim() != 2 or mean.shape[0] != N:
+        raise ValueError("mean must have shape (N, G)")
+    G = mean.shape[-1]
+    if C > 0:
+        _check_groups(C, G)
+    ok = _stat(mean, N * G, "mean", dy) and ok
+    ok = _stat(rstd, N * G, "rstd", dy) and ok
+    ok = _affine_ok(weight, C, dy.device, "weight") and ok
+    ok = _affine_ok(bias, C, dy.device, "bias") and ok
+    affine = _affine_flag(weight, bias)
+    if not ok or affine is None or C == 0 or C > MAX_CHANNELS or not dy.is_contiguous():
+        return None
+    if xp is not None and not x.is_contiguous():
+        return None
+    if out is None:
+        out = _dense_like(dy)
+    else:
+        _check_out(out, dy)
+        if not out.is_contiguous():
+            raise ValueError("out must be contiguous")
+    dw, db = _weight_gradients(weight if weight is not None else bias, C, dy, weight_grad)
+    if N * L == 0:
+        if weight_grad:
+            dw.zero_()
+            db.zero_()
+        return out, dw, db
+    dtype = dtype_code(dy.dtype) | affine
+    need = _i64(0)
+    code = lib.gn_silu_rows_backward_workspace(N, L, C, G, dtype, ctypes.byref(need))
+    if _result(code, True) is None:
+        return None
+    ws = torch.empty(need.value, dtype=torch.uint8, device=dy.device)
+    code = lib.gn_silu_rows_backward(
+        _addr(dy), xp, codes, scales, _addr(mean), _addr(rstd), _addr(weight), _addr(bias), _addr(out),
+        _addr(dw), _addr(db), N, L, C, G, 1 if apply_silu else 0, dtype, _addr(ws), need.value,
+        _stream_handle(dy))
+    return _result(code, (out, dw, db))
 
 
 PLAN_FIELDS = ("slots", "tiles", "full", "tpc1", "K1", "tpc2", "K2", "scratch_bytes",

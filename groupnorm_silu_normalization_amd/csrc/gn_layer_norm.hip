@@ -1,0 +1,602 @@
+// gn_layer_norm.hip -- layer norm over the last dimension of rows, forward and
+// backward, for MI355X (gfx950).
+//
+//   forward    mean = sum(x)/C, var = sum((x-mean)^2)/C, rstd = 1/sqrt(var+eps),
+//              y = gamma*(x-mean)*rstd + beta
+//   backward   h = (x-mean)*rstd, g = dy*gamma,
+//              dx = rstd*(g - sum(g)/C - h*sum(g*h)/C),
+//              dgamma[c] = sum over rows of dy*h, dbeta[c] = sum over rows of dy
+//
+// Both passes are bound by HBM: a row is read once, held in registers and
+// written once.  A row belongs to TPR lanes (a power of two within a wave, or
+// a whole workgroup), each holding NV pieces of W channels, so the two sums of
+// a row are a lane-group butterfly (plus, for a workgroup, one exchange of the
+// waves' sums through LDS).  The mean is taken first and the variance from the
+// differences: with the row in registers the second sum costs no memory
+// traffic, and no channel far from the rest can cancel it.
+//
+// The weight's gradients run down the columns.  A lane keeps the same channels
+// for every row it works on, so their sums stay in its registers over all of a
+// workgroup's rows; the workgroup adds its row slots in a fixed order and
+// writes one partial row of C sums, and a second kernel adds the partial rows
+// (in fp64) in a fixed order: no atomics, the same bits on every call.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <type_traits>
+
+#include "gn_host.hpp"
+#include "gn_rows.hpp"
+#include "gnsilu.h"
+
+namespace gnsilu {
+namespace {
+
+struct LnArgs {
+    const void *x;          // rows of x, or null when codes/scales hold them
+    const int8_t *codes;    // [M][C]
+    const uint8_t *scales;  // [M][ceil(C / 32)]
+    const void *dy;
+    void *y;                // forward: y; backward: dx
+    int8_t *codes_out;      // forward: the checkpoint, or null
+    uint8_t *scales_out;
+    float *mean, *rstd;     // [M]; forward: written unless null, backward: read
+    float *part;            // backward: [2][blocks][C] partial dgamma, dbeta, or null
+    int64_t M, x_stride, dy_stride, y_stride;
+    int C, P;
+    float eps;
+    Affine af;
+};
+
+// The sum over a row's lanes.  A workgroup's row (TPR > 64) exchanges the
+// waves' sums through `red`; the caller passes a different part of it to
+// consecutive sums, so one barrier is enough.
+template <int TPR, int K>
+__device__ __forceinline__ void row_sum(float (&v)[K], float *red) {
+    constexpr int N = TPR < 64 ? TPR : 64;
+#pragma unroll
+    for (int k = 0; k < K; ++k) v[k] = lane_sum<N>(v[k]);
+    if constexpr (TPR > 64) {
+        constexpr int kWaves = TPR / 64;
+        const int wave = threadIdx.x >> 6;
+        if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+            for (int k = 0; k < K; ++k) red[k * kWaves + wave] = v[k];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            float s = red[k * kWaves];
+#pragma unroll
+            for (int w = 1; w < kWaves; ++w) s += red[k * kWaves + w];
+            v[k] = s;
+        }
+    }
+}
+
+// Where the calling lane's piece j starts in its row and its first own
+// channel; W for a lane beyond the row (it reads piece 0 and counts nothing).
+template <int W, bool TAIL>
+__device__ __forceinline__ void piece_at(const LnArgs &a, int p, int *c, int *lo) {
+    *lo = 0;
+    *c = p * W;
+    if (p >= a.P) {
+        *c = 0;
+        *lo = W;
+    } else if (TAIL && *c + W > a.C) {
+        *lo = *c + W - a.C;
+        *c = a.C - W;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Forward.  Row slots per workgroup: THREADS / TPR.
+// ---------------------------------------------------------------------------
+template <class D, int W, bool TAIL, int TPR, int NV, int THREADS, bool SAVE>
+__global__ __launch_bounds__(THREADS) void gn_layer_norm(LnArgs a) {
+    using T = typename D::storage;
+    constexpr int kSlots = THREADS / TPR;
+    constexpr int kRed = TPR > 64 ? TPR / 64 : 1;
+    constexpr int kGroup = TPR < kBlock8 / W ? TPR : kBlock8 / W;
+    __shared__ float red[2 * kRed];
+    const int t = threadIdx.x % TPR, slot = threadIdx.x / TPR;
+    const T *x = static_cast<const T *>(a.x);
+    T *y = static_cast<T *>(a.y);
+    int c[NV], lo[NV];
+    float ga[NV][W], be[NV][W];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        piece_at<W, TAIL>(a, t + j * TPR, &c[j], &lo[j]);
+        load_affine<W>(a.af.gamma, a.af.type, c[j], 1.0f, ga[j]);
+        load_affine<W>(a.af.beta, a.af.type, c[j], 0.0f, be[j]);
+    }
+    const float fc = static_cast<float>(a.C);
+    const int64_t nsb = (a.C + kBlock8 - 1) / kBlock8;
+    for (int64_t base = int64_t{blockIdx.x} * kSlots; base < a.M;
+         base += int64_t{gridDim.x} * kSlots) {
+        const bool live = base + slot < a.M;
+        const int64_t m = live ? base + slot : a.M - 1;
+        Piece<D, W> v[NV];
+#pragma unroll
+        for (int j = 0; j < NV; ++j) v[j].template load<false>(x + m * a.x_stride + c[j]);
+        float s[1] = {0.0f};
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int i = 0; i < W; ++i) s[0] += i >= lo[j] ? v[j].get(i) : 0.0f;
+        row_sum<TPR>(s, red);
+        const float mean = s[0] / fc;
+        float q[1] = {0.0f};
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int i = 0; i < W; ++i) {
+                const float d = i >= lo[j] ? v[j].get(i) - mean : 0.0f;
+                q[0] = fmaf(d, d, q[0]);
+            }
+        row_sum<TPR>(q, red + kRed);
+        const float rstd = 1.0f / sqrtf(q[0] / fc + a.eps);
+        if (live && t == 0) {
+            if (a.mean != nullptr) a.mean[m] = mean;
+            if (a.rstd != nullptr) a.rstd[m] = rstd;
+        }
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            float f[W], o[W];
+#pragma unroll
+            for (int i = 0; i < W; ++i) {
+                f[i] = v[j].get(i);
+                o[i] = fmaf((f[i] - mean) * rstd, ga[j][i], be[j][i]);
+            }
+            // A last piece's foreign channels get the value that their owner
+            // writes, computed alike.
+            if (live && lo[j] < W) Piece<D, W>::template store<false>(y + m * a.y_stride + c[j], o);
+            if constexpr (SAVE) {
+                const uint32_t E = block8_exponent<W, kGroup>(f, lo[j]);
+                const Codes<W> qd = block8_encode<W>(f, E);
+                if (live && lo[j] < W)
+                    store_block8<W, TAIL>(qd, E, a.codes_out, a.scales_out, m * a.C, m * nsb,
+                                          c[j], lo[j]);
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Backward.  SAVED: x comes from its 8-bit checkpoint.
+// ---------------------------------------------------------------------------
+template <class D, int W, bool TAIL, int TPR, int NV, int THREADS, bool SAVED>
+__global__ __launch_bounds__(THREADS) void gn_layer_norm_backward(LnArgs a) {
+    using T = typename D::storage;
+    constexpr int kSlots = THREADS / TPR;
+    constexpr int kRed = TPR > 64 ? 2 * (TPR / 64) : 1;
+    __shared__ float red[2 * kRed];
+    const int t = threadIdx.x % TPR, slot = threadIdx.x / TPR;
+    const T *x = static_cast<const T *>(a.x);
+    const T *dy = static_cast<const T *>(a.dy);
+    T *dx = static_cast<T *>(a.y);
+    int c[NV], lo[NV];
+    float ga[NV][W], dg[NV][W], db[NV][W];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        piece_at<W, TAIL>(a, t + j * TPR, &c[j], &lo[j]);
+        load_affine<W>(a.af.gamma, a.af.type, c[j], 1.0f, ga[j]);
+#pragma unroll
+        for (int i = 0; i < W; ++i) dg[j][i] = db[j][i] = 0.0f;
+    }
+    const float fc = static_cast<float>(a.C);
+    const int64_t nsb = (a.C + kBlock8 - 1) / kBlock8;
+    int par = 0;
+    for (int64_t base = int64_t{blockIdx.x} * kSlots; base < a.M;
+         base += int64_t{gridDim.x} * kSlots) {
+        const bool live = base + slot < a.M;
+        const int64_t m = live ? base + slot : a.M - 1;
+        Piece<D, W> vx[NV], vy[NV];
+        Piece8<W, TAIL> v8[NV];
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            if constexpr (SAVED)
+                v8[j].load(a.codes, a.scales, m * a.C, m * nsb, c[j]);
+            else
+                vx[j].template load<false>(x + m * a.x_stride + c[j]);
+            vy[j].template load<false>(dy + m * a.dy_stride + c[j]);
+        }
+        const float mean = a.mean[m], rstd = a.rstd[m];
+        float h[NV][W];
+        float s[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            if constexpr (SAVED) v8[j].widen(c[j], h[j]);
+#pragma unroll
+            for (int i = 0; i < W; ++i) {
+                const float xv = SAVED ? h[j][i] : vx[j].get(i);
+                h[j][i] = (xv - mean) * rstd;
+                const float g = i >= lo[j] ? vy[j].get(i) * ga[j][i] : 0.0f;
+                s[0] += g;
+                // a select, not a product with a zero g: h may be NaN there
+                s[1] += i >= lo[j] ? g * h[j][i] : 0.0f;
+            }
+        }
+        row_sum<TPR>(s, red + par * kRed);
+        par ^= 1;
+        const float s0 = s[0] / fc, s1 = s[1] / fc;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            float o[W];
+#pragma unroll
+            for (int i = 0; i < W; ++i) {
+                const float d = vy[j].get(i);
+                o[i] = rstd * fmaf(-h[j][i], s1, fmaf(d, ga[j][i], -s0));
+                dg[j][i] = live ? fmaf(d, h[j][i], dg[j][i]) : dg[j][i];
+                db[j][i] = live ? db[j][i] + d : db[j][i];
+            }
+            if (live && lo[j] < W) Piece<D, W>::template store<false>(dx + m * a.y_stride + c[j], o);
+        }
+    }
+    if (a.part == nullptr) return;
+    // The row slots of the workgroup: within a wave by butterflies over the
+    // lanes that hold the same channels, then wave by wave through LDS.
+    float *pg = a.part + int64_t{blockIdx.x} * a.C;
+    float *pb = pg + int64_t{gridDim.x} * a.C;
+    if constexpr (TPR >= 64) {
+        constexpr int kWaveSlots = kSlots;  // waves that hold the same channels
+        __shared__ float comb[kWaveSlots > 1 ? 2 * NV * W * 64 : 1];
+#pragma unroll 1
+        for (int w = 0; w < kWaveSlots; ++w) {
+            if (slot == w) {
+#pragma unroll
+                for (int j = 0; j < NV; ++j)
+#pragma unroll
+                    for (int i = 0; i < W; ++i) {
+                        const int e = (j * W + i) * 64 + (threadIdx.x & 63);
+                        if constexpr (kWaveSlots > 1) {
+                            if (w > 0) {
+                                dg[j][i] += comb[e];
+                                db[j][i] += comb[NV * W * 64 + e];
+                            }
+                            if (w + 1 < kWaveSlots) {
+                                comb[e] = dg[j][i];
+                                comb[NV * W * 64 + e] = db[j][i];
+                            }
+                        }
+                        if (w + 1 == kWaveSlots && i >= lo[j]) {
+                            pg[c[j] + i] = dg[j][i];
+                            pb[c[j] + i] = db[j][i];
+                        }
+                    }
+            }
+            if constexpr (kWaveSlots > 1) __syncthreads();
+        }
+    } else {
+        static_assert(NV == 1, "rows of fewer lanes than a wave have one piece per lane");
+        constexpr int kWaves = THREADS / 64;
+        __shared__ float comb[2][kWaves][W][TPR];
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            float g = dg[0][i], b = db[0][i];
+#pragma unroll
+            for (int o = TPR; o < 64; o <<= 1) {
+                g += __shfl_xor(g, o, 64);
+                b += __shfl_xor(b, o, 64);
+            }
+            if ((threadIdx.x & 63) < TPR) {
+                comb[0][threadIdx.x >> 6][i][t] = g;
+                comb[1][threadIdx.x >> 6][i][t] = b;
+            }
+        }
+        __syncthreads();
+        if (threadIdx.x < TPR) {
+#pragma unroll
+            for (int i = 0; i < W; ++i) {
+                float g = comb[0][0][i][t], b = comb[1][0][i][t];
+#pragma unroll
+                for (int w = 1; w < kWaves; ++w) {
+                    g += comb[0][w][i][t];
+                    b += comb[1][w][i][t];
+                }
+                if (i >= lo[0]) {
+                    pg[c[0] + i] = g;
+                    pb[c[0] + i] = b;
+                }
+            }
+        }
+    }
+}
+
+// dgamma and dbeta from the K partial rows of C sums: 64 channels and 16 row
+// parts per workgroup, each part's rows in order, then the parts in order, in
+// fp64.  K = 0 writes zeros.  blockIdx.y: 0 dgamma, 1 dbeta.
+constexpr int kColParts = 16;
+__global__ __launch_bounds__(64 * kColParts) void gn_column_sums(const float *part, int64_t K, int C,
+                                                                 void *dgamma, void *dbeta,
+                                                                 int type) {
+    __shared__ double red[kColParts][64];
+    void *out = blockIdx.y == 0 ? dgamma : dbeta;
+    if (out == nullptr) return;
+    const int lane = threadIdx.x & 63, r = threadIdx.x >> 6;
+    const int c = static_cast<int>(blockIdx.x) * 64 + lane;
+    const float *p = part + static_cast<int64_t>(blockIdx.y) * K * C;
+    double s = 0.0;
+    if (c < C) {
+#pragma unroll 8
+        for (int64_t k = r; k < K; k += kColParts) s += static_cast<double>(p[k * C + c]);
+    }
+    red[r][lane] = s;
+    __syncthreads();
+    if (r == 0 && c < C) {
+#pragma unroll
+        for (int i = 1; i < kColParts; ++i) s += red[i][lane];
+        store_affine(out, type, c, static_cast<float>(s));
+    }
+}
+
+// ---- host -----------------------------------------------------------------------
+constexpr int64_t kForwardBlocks = 2048;   // workgroups of 256 lanes: 8 per CU
+constexpr int64_t kBackwardBlocks = 512;   // 2 per CU: each writes a partial row
+
+// Lanes and pieces of a row: the fewest lanes of a wave that hold it with one
+// piece each, then up to four pieces per lane, then a workgroup per row.
+struct LnShape {
+    int w, tpr, nv, threads;
+    bool tail;
+    int P;
+    int slots() const { return threads / tpr; }
+};
+
+LnShape ln_shape(int64_t C, int dtype) {
+    LnShape s;
+    const int w = static_cast<int>(16 / elem_bytes(dtype));
+    s.w = C < w ? 1 : w;
+    s.tail = C % s.w != 0;
+    s.P = static_cast<int>(ceil_div(C, s.w));
+    s.threads = 256;
+    if (s.P <= 64) {
+        s.nv = 1;
+        s.tpr = 1;
+        while (s.tpr < s.P) s.tpr *= 2;
+        if (s.w == 1) s.tpr = 8;
+    } else if (s.P <= 256) {
+        s.tpr = 64;
+        s.nv = s.P <= 128 ? 2 : 4;
+    } else if (s.P <= 1024) {
+        s.tpr = 256;
+        s.nv = s.P <= 512 ? 2 : 4;
+    } else {
+        s.tpr = s.threads = 512;
+        s.nv = s.P <= 2048 ? 4 : 8;
+    }
+    return s;
+}
+
+template <int V> using IC = std::integral_constant<int, V>;
+
+// Calls f(IC<W>, IC<TAIL>, IC<TPR>, IC<NV>, IC<THREADS>).
+template <class D, class F>
+void with_ln_shape(const LnShape &s, F &&f) {
+    constexpr int W = static_cast<int>(16 / sizeof(typename D::storage));
+    if (s.w == 1) {
+        f(IC<1>{}, IC<0>{}, IC<8>{}, IC<1>{}, IC<256>{});
+        return;
+    }
+    auto by_tail = [&](auto tail) {
+        if (s.tpr == 512) {
+            if (s.nv == 4)
+                f(IC<W>{}, tail, IC<512>{}, IC<4>{}, IC<512>{});
+            else if constexpr (W == 4)
+                f(IC<W>{}, tail, IC<512>{}, IC<8>{}, IC<512>{});
+            return;
+        }
+        if (s.tpr == 256) {
+            if (s.nv == 2)
+                f(IC<W>{}, tail, IC<256>{}, IC<2>{}, IC<256>{});
+            else
+                f(IC<W>{}, tail, IC<256>{}, IC<4>{}, IC<256>{});
+            return;
+        }
+        if (s.nv == 4) return f(IC<W>{}, tail, IC<64>{}, IC<4>{}, IC<256>{});
+        if (s.nv == 2) return f(IC<W>{}, tail, IC<64>{}, IC<2>{}, IC<256>{});
+        switch (s.tpr) {
+            case 1: return f(IC<W>{}, IC<0>{}, IC<1>{}, IC<1>{}, IC<256>{});  // P = 1: C = W
+            case 2: return f(IC<W>{}, tail, IC<2>{}, IC<1>{}, IC<256>{});
+            case 4: return f(IC<W>{}, tail, IC<4>{}, IC<1>{}, IC<256>{});
+            case 8: return f(IC<W>{}, tail, IC<8>{}, IC<1>{}, IC<256>{});
+            case 16: return f(IC<W>{}, tail, IC<16>{}, IC<1>{}, IC<256>{});
+            case 32: return f(IC<W>{}, tail, IC<32>{}, IC<1>{}, IC<256>{});
+            default: return f(IC<W>{}, tail, IC<64>{}, IC<1>{}, IC<256>{});
+        }
+    };
+    if (s.tail)
+        by_tail(IC<1>{});
+    else
+        by_tail(IC<0>{});
+}
+
+template <class D>
+void launch_forward(const LnShape &s, const LnArgs &a, hipStream_t st) {
+    const int64_t blocks = std::min(ceil_div(a.M, s.slots()), kForwardBlocks * 256 / s.threads);
+    with_ln_shape<D>(s, [&](auto w, auto tail, auto tpr, auto nv, auto nt) {
+        constexpr int W = decltype(w)::value, TPR = decltype(tpr)::value;
+        constexpr int NV = decltype(nv)::value, NT = decltype(nt)::value;
+        constexpr bool TAIL = decltype(tail)::value != 0;
+        const dim3 grid(static_cast<unsigned>(blocks)), block(NT);
+        if (a.codes_out != nullptr)
+            gn_layer_norm<D, W, TAIL, TPR, NV, NT, true><<<grid, block, 0, st>>>(a);
+        else
+            gn_layer_norm<D, W, TAIL, TPR, NV, NT, false><<<grid, block, 0, st>>>(a);
+    });
+}
+
+int64_t backward_blocks(const LnShape &s, int64_t M) {
+    return std::min(ceil_div(M, s.slots()), kBackwardBlocks * 256 / s.threads);
+}
+
+template <class D>
+void launch_backward(const LnShape &s, const LnArgs &a, hipStream_t st) {
+    const int64_t blocks = backward_blocks(s, a.M);
+    with_ln_shape<D>(s, [&](auto w, auto tail, auto tpr, auto nv, auto nt) {
+        constexpr int W = decltype(w)::value, TPR = decltype(tpr)::value;
+        constexpr int NV = decltype(nv)::value, NT = decltype(nt)::value;
+        constexpr bool TAIL = decltype(tail)::value != 0;
+        const dim3 grid(static_cast<unsigned>(blocks)), block(NT);
+        if (a.codes != nullptr)
+            gn_layer_norm_backward<D, W, TAIL, TPR, NV, NT, true><<<grid, block, 0, st>>>(a);
+        else
+            gn_layer_norm_backward<D, W, TAIL, TPR, NV, NT, false><<<grid, block, 0, st>>>(a);
+    });
+}
+
+template <class F>
+void by_type(int dtype, F &&f) {
+    switch (x_dtype(dtype)) {
+        case GN_DTYPE_F16: f(Fp16{}); break;
+        case GN_DTYPE_F32: f(F32{}); break;
+        default: f(Bf16{}); break;
+    }
+}
+
+bool overflows(int64_t M, int64_t stride, int64_t C) {
+    return M > 0 && stride > 0 && M > (INT64_MAX / 4 - C) / stride;
+}
+
+bool misaligned(const void *p, int64_t bytes) {
+    return (reinterpret_cast<uintptr_t>(p) & static_cast<uintptr_t>(bytes - 1)) != 0;
+}
+
+// The checks both passes share; in_strides: row strides of inputs (0: one row
+// for all), out_stride: of the output.
+gn_status check_ln(int64_t M, int64_t C, int dtype, const int64_t *in_strides, int n_in,
+                   int64_t out_stride) {
+    if (!valid_dtype(dtype)) return GN_INVALID_ARGUMENT;
+    if (M < 0 || C <= 0) return GN_INVALID_ARGUMENT;
+    if (overflows(M, C, C)) return GN_INVALID_ARGUMENT;
+    for (int i = 0; i < n_in; ++i) {
+        if (in_strides[i] < 0) return GN_INVALID_ARGUMENT;
+        if (overflows(M, in_strides[i], C)) return GN_INVALID_ARGUMENT;
+    }
+    if (out_stride < 0 || (M > 1 && out_stride < C)) return GN_INVALID_ARGUMENT;
+    if (overflows(M, out_stride, C)) return GN_INVALID_ARGUMENT;
+    if (C > GN_LAYER_NORM_MAX_CHANNELS) return GN_UNSUPPORTED;
+    return GN_OK;
+}
+
+size_t backward_workspace(int64_t M, int64_t C, int dtype) {
+    if (M == 0) return 0;
+    return sizeof(float) * 2 * static_cast<size_t>(backward_blocks(ln_shape(C, dtype), M)) *
+           static_cast<size_t>(C);
+}
+
+}  // namespace
+}  // namespace gnsilu
+
+using namespace gnsilu;
+
+extern "C" {
+
+gn_status gn_layer_norm_rows(const void *x, int64_t x_stride, const void *gamma, const void *beta,
+                             void *y, int64_t y_stride, int64_t M, int64_t C, float eps, int dtype,
+                             float *mean_out, float *rstd_out, void *codes_out, void *scales_out,
+                             void *stream) {
+    if (x == nullptr || y == nullptr) return GN_INVALID_ARGUMENT;
+    if ((codes_out == nullptr) != (scales_out == nullptr)) return GN_INVALID_ARGUMENT;
+    if (!(eps >= 0.0f) || std::isinf(eps)) return GN_INVALID_ARGUMENT;
+    gn_status st = check_ln(M, C, dtype, &x_stride, 1, y_stride);
+    if (st == GN_OK) st = check_affine(gamma, beta, dtype);
+    if (st != GN_OK) return st;
+    const int64_t es = elem_bytes(dtype);
+    if (misaligned(x, es) || misaligned(y, es) || misaligned(mean_out, 4) ||
+        misaligned(rstd_out, 4))
+        return GN_UNSUPPORTED;
+    if (M == 0) return GN_OK;
+    Call c;
+    st = begin_call(stream,
+                    {x, gamma, beta, y, mean_out, rstd_out, codes_out, scales_out}, &c);
+    if (st != GN_OK) return st;
+    const LnShape s = ln_shape(C, dtype);
+    LnArgs a{};
+    a.x = x;
+    a.y = y;
+    a.codes_out = static_cast<int8_t *>(codes_out);
+    a.scales_out = static_cast<uint8_t *>(scales_out);
+    a.mean = mean_out;
+    a.rstd = rstd_out;
+    a.M = M;
+    a.x_stride = x_stride;
+    a.y_stride = y_stride;
+    a.C = static_cast<int>(C);
+    a.P = s.P;
+    a.eps = eps;
+    a.af = Affine{gamma, beta, affine_type(dtype)};
+    by_type(dtype, [&](auto d) { launch_forward<decltype(d)>(s, a, c.stream); });
+    return finish_launch();
+}
+
+gn_status gn_layer_norm_rows_backward_workspace(int64_t M, int64_t C, int dtype,
+                                                int64_t *bytes_out) {
+    if (bytes_out == nullptr) return GN_INVALID_ARGUMENT;
+    const gn_status st = check_ln(M, C, dtype, nullptr, 0, C);
+    if (st != GN_OK) return st;
+    *bytes_out = static_cast<int64_t>(backward_workspace(M, C, dtype));
+    return GN_OK;
+}
+
+gn_status gn_layer_norm_rows_backward(const void *dy, int64_t dy_stride, const void *x,
+                                      int64_t x_stride, const void *codes, const void *scales,
+                                      const float *mean, const float *rstd, const void *gamma,
+                                      void *dx, int64_t dx_stride, void *dgamma, void *dbeta,
+                                      int64_t M, int64_t C, int dtype, void *workspace,
+                                      int64_t workspace_bytes, void *stream) {
+    if (dy == nullptr || dx == nullptr || mean == nullptr || rstd == nullptr)
+        return GN_INVALID_ARGUMENT;
+    // x, or its checkpoint, not both
+    if ((codes == nullptr) != (scales == nullptr) || (x == nullptr) == (codes == nullptr))
+        return GN_INVALID_ARGUMENT;
+    const int64_t strides[2] = {dy_stride, x == nullptr ? 0 : x_stride};
+    gn_status st = check_ln(M, C, dtype, strides, 2, dx_stride);
+    if (st == GN_OK) st = check_affine(gamma, nullptr, dtype);
+    if (st == GN_OK) st = check_affine(dgamma, dbeta, dtype);
+    if (st != GN_OK) return st;
+    const int64_t es = elem_bytes(dtype);
+    if (misaligned(dy, es) || misaligned(x, es) || misaligned(dx, es) || misaligned(mean, 4) ||
+        misaligned(rstd, 4) || misaligned(workspace, 4))
+        return GN_UNSUPPORTED;
+    const bool grads = dgamma != nullptr || dbeta != nullptr;
+    if (M == 0 && !grads) return GN_OK;
+    const size_t need = grads ? backward_workspace(M, C, dtype) : 0;
+    if (need > 0 && workspace == nullptr) return GN_INVALID_ARGUMENT;
+    if (need > 0 && (workspace_bytes < 0 || static_cast<size_t>(workspace_bytes) < need))
+        return GN_SCRATCH_TOO_SMALL;
+    Call c;
+    st = begin_call(stream,
+                    {dy, x, codes, scales, mean, rstd, gamma, dx, dgamma, dbeta,
+                     need > 0 ? workspace : nullptr},
+                    &c);
+    if (st != GN_OK) return st;
+    const LnShape s = ln_shape(C, dtype);
+    LnArgs a{};
+    a.x = x;
+    a.codes = static_cast<const int8_t *>(codes);
+    a.scales = static_cast<const uint8_t *>(scales);
+    a.dy = dy;
+    a.y = dx;
+    a.mean = const_cast<float *>(mean);
+    a.rstd = const_cast<float *>(rstd);
+    a.part = grads ? static_cast<float *>(workspace) : nullptr;
+    a.M = M;
+    a.x_stride = x_stride;
+    a.dy_stride = dy_stride;
+    a.y_stride = dx_stride;
+    a.C = static_cast<int>(C);
+    a.P = s.P;
+    a.af = Affine{gamma, nullptr, affine_type(dtype)};
+    if (M > 0) by_type(dtype, [&](auto d) { launch_backward<decltype(d)>(s, a, c.stream); });
+    if (grads)
+        gn_column_sums<<<dim3(static_cast<unsigned>(ceil_div(C, 64)), 2), 64 * kColParts, 0,
+                         c.stream>>>(static_cast<const float *>(workspace),
+                                     M > 0 ? backward_blocks(s, M) : 0, a.C, dgamma, dbeta,
+                                     a.af.type);
+    return finish_launch();
+}
+
+}  // extern "C"

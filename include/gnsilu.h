@@ -100,7 +100,7 @@ typedef enum gn_status {
     GN_UNSUPPORTED = 1,
     GN_INVALID_ARGUMENT = 2,
     GN_DEVICE_ERROR = 3,
-    GN_SCRATCH_TOO_SMALL = 4  /* gn_silu_rows_noalloc only: see there */
+    GN_SCRATCH_TOO_SMALL = 4  /* gn_silu_rows_noalloc, *_backward: see there */
 } gn_status;
 
 /* Element type of x and y for the *_dtype entry points.  The page's kernel
@@ -334,6 +334,107 @@ gn_status gn_profile_rows_dtype(const void *x, const float *gamma, const float *
                                 int iters, float *kernel_ms, int *n_kernels);
 gn_status gn_plan_rows_dtype(int64_t N, int64_t L, int64_t C, int64_t G, int dtype,
                              int64_t plan_out[15]);
+
+/* Layer norm, the backward passes and 8-bit checkpoints ------------------------
+ *
+ * The entry points below share the conventions above, with these differences:
+ * - Alignment: x, dy, y, dx need only their element's alignment, and every C
+ *   up to the stated limit is supported, so a row may start anywhere.
+ * - Rows may be apart: *_stride is the number of elements from one row's
+ *   first value to the next one's.  Rows of an input may coincide (stride 0:
+ *   one row for all) or overlap; an output's stride is at least C when there
+ *   is more than one row (else GN_INVALID_ARGUMENT).
+ * - Workspace: calls that need one take it from the caller (its size in bytes
+ *   from the matching *_workspace call; device memory, 4-byte aligned; too
+ *   small: GN_SCRATCH_TOO_SMALL; null where one is needed:
+ *   GN_INVALID_ARGUMENT).  Its contents before a call are irrelevant; it must
+ *   stay valid and unused by other work until the stream has executed the
+ *   call.  Two calls that may overlap need a workspace each; a captured graph
+ *   keeps using the one it was captured with.
+ * - Aliasing: y == x and dx == x or dx == dy with the same stride are allowed
+ *   (the whole row or element is read before it is written).
+ * - dtype is the gn_dtype of x, y, dy and dx, or-ed with the GN_AFFINE_* type
+ *   of gamma, beta, dgamma and dbeta (none: fp32).  dgamma and dbeta are
+ *   summed in fp32 and fp64 in a fixed order and rounded once; either may be
+ *   null (not wanted).  An empty input gives zeros in them and enqueues
+ *   nothing else.
+ *
+ * 8-bit checkpoints.  A forward pass may keep its input in 8 bits for the
+ * backward pass.  Blocks of GN_CHECKPOINT_BLOCK consecutive channels of a row
+ * (the row's last block may be shorter) share a scale byte E, the exponent
+ * field (biased by 127; 0 for zero and subnormals) of the block's largest
+ * magnitude as an fp32 number; a value x is kept as the code
+ *     q = clamp(round_half_even(x * 2^(133-E)), -127, 127)
+ * and stands for q * 2^(E-133) (elements and scales of the OCP MX format
+ * MXINT8).  The error is at most 2^(E-134), one part in 128 of the block's
+ * largest magnitude, and 2^(E-133) for magnitudes in the topmost half step of
+ * the block's range, which the clamp takes.  Scaling by powers of two is
+ * exact, so the codes depend on x alone.  A block that holds an infinity or a
+ * NaN has E = 255 and stands for NaN throughout.  codes: int8 [M][C], scales:
+ * uint8 [M][ceil(C / GN_CHECKPOINT_BLOCK)], dense, any alignment: 1 + 1/32
+ * bytes per value. */
+#define GN_CHECKPOINT_BLOCK 32
+#define GN_LAYER_NORM_MAX_CHANNELS 16384
+
+/* Saves M rows of C values (C <= GN_LAYER_NORM_MAX_CHANNELS) in 8 bits, and
+ * widens saved rows again (rounded once to dtype). */
+gn_status gn_checkpoint_rows(const void *x, int64_t x_stride, void *codes, void *scales, int64_t M,
+                             int64_t C, int dtype, void *stream);
+gn_status gn_restore_rows(const void *codes, const void *scales, void *x, int64_t x_stride,
+                          int64_t M, int64_t C, int dtype, void *stream);
+
+/* Layer norm of M rows of C values, C <= GN_LAYER_NORM_MAX_CHANNELS:
+ *     mean = sum(x)/C, var = sum((x-mean)^2)/C, rstd = 1/sqrt(var + eps)
+ *     y = gamma*(x-mean)*rstd + beta
+ * mean_out / rstd_out: fp32 [M] or null.  codes / scales: the checkpoint of x,
+ * both or neither, written in the same pass. */
+gn_status gn_layer_norm_rows(const void *x, int64_t x_stride, const void *gamma, const void *beta,
+                             void *y, int64_t y_stride, int64_t M, int64_t C, float eps, int dtype,
+                             float *mean_out, float *rstd_out, void *codes_out, void *scales_out,
+                             void *stream);
+
+/* Its backward pass, with mean and rstd as gn_layer_norm_rows wrote them:
+ *     h = (x-mean)*rstd, g = dy*gamma
+ *     dx = rstd*(g - sum(g)/C - h*sum(g*h)/C)
+ *     dgamma[c] = sum over rows of dy*h, dbeta[c] = sum over rows of dy
+ * The input comes as x or as its checkpoint (codes and scales), the other
+ * null; with a checkpoint the formulas hold for the values it stands for.
+ * The workspace is needed only when dgamma or dbeta is. */
+gn_status gn_layer_norm_rows_backward_workspace(int64_t M, int64_t C, int dtype,
+                                                int64_t *bytes_out);
+gn_status gn_layer_norm_rows_backward(const void *dy, int64_t dy_stride, const void *x,
+                                      int64_t x_stride, const void *codes, const void *scales,
+                                      const float *mean, const float *rstd, const void *gamma,
+                                      void *dx, int64_t dx_stride, void *dgamma, void *dbeta,
+                                      int64_t M, int64_t C, int dtype, void *workspace,
+                                      int64_t workspace_bytes, void *stream);
+
+/* Step three that also writes the checkpoint of x, for dense (N, L, C) rows of
+ * any C <= GN_MAX_CHANNELS.  y is gn_apply_rows_dtype's bit for bit in bf16
+ * and fp32; in fp16, where the last product of a value that a kernel stores
+ * alone is rounded once and that of one in a wide access twice, a value may
+ * differ by one fp16 step. */
+gn_status gn_apply_rows_save(const void *x, const float *mean, const float *rstd,
+                             const void *gamma, const void *beta, void *y, void *codes,
+                             void *scales, int64_t N, int64_t L, int64_t C, int64_t G,
+                             int apply_silu, int dtype, void *stream);
+
+/* The backward pass of GroupNorm(+SiLU) over dense (N, L, C) rows, any
+ * C <= GN_MAX_CHANNELS, with mean and rstd [N][G] as gn_stats_rows wrote them:
+ *     h = (x-mean)*rstd, t = gamma*h + beta, s = sigmoid(t)
+ *     dt = apply_silu ? dy*s*(1 + t*(1-s)) : dy
+ *     dgamma[c] = sum over n, l of dt*h, dbeta[c] = sum over n, l of dt
+ *     a, b = means over the group (L*C/G values) of gamma*dt and gamma*dt*h
+ *     dx = rstd*(gamma*dt - a - h*b)
+ * The input comes as x or as its checkpoint, as for layer norm. */
+gn_status gn_silu_rows_backward_workspace(int64_t N, int64_t L, int64_t C, int64_t G, int dtype,
+                                          int64_t *bytes_out);
+gn_status gn_silu_rows_backward(const void *dy, const void *x, const void *codes,
+                                const void *scales, const float *mean, const float *rstd,
+                                const void *gamma, const void *beta, void *dx, void *dgamma,
+                                void *dbeta, int64_t N, int64_t L, int64_t C, int64_t G,
+                                int apply_silu, int dtype, void *workspace,
+                                int64_t workspace_bytes, void *stream);
 
 /* The GroupNorm(+SiLU) fused into the neighbouring 3x3 convolution of the
  * decoder's ResnetBlock2D (Modifications section 2: "ResnetBlock2D
