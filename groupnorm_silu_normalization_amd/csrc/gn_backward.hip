@@ -34,14 +34,17 @@ namespace gnsilu {
 namespace {
 
 constexpr int kLanes = 256;
+constexpr int kSumLanes = 512;  // pass 1 beyond kSmallBytes
+constexpr int kUnroll = 2;      // tiles per batch; two batches of loads are in flight ...
+constexpr int kInputUnroll = 4; // ... in pass 2 from x itself
 
 struct Tiles {
-    int64_t L;    // rows per sample
-    int64_t K;    // chunks per sample
-    int64_t rpc;  // rows per chunk (the last one may be shorter)
-    int C, P;     // channels and pieces of a row
-    int ncb, Pc;  // column blocks of a row and their pieces
-    int R;        // rows per tile
+    int64_t L;        // rows per sample
+    int64_t batches;  // batches of U tiles per sample (the last one may be partial)
+    int64_t K;        // workgroups per sample and column block: every K-th batch is one's own
+    int C, P;         // channels and pieces of a row
+    int ncb, Pc;      // column blocks of a row and their pieces
+    int R;            // rows per tile
 };
 
 struct RowArgs {
@@ -61,20 +64,20 @@ struct RowArgs {
     Tiles tl;
 };
 
-// The calling lane's rows and piece.
+// The calling lane's sample, workgroup of the sample, row slot and piece.
 template <int W, bool TAIL> struct Place {
-    int64_t n, k, l, l1;  // sample, chunk, first row, end of the chunk's rows
+    int64_t n, k;
     int r, c, lo;
     bool active;
     __device__ __forceinline__ explicit Place(const Tiles &t) {
-        const int64_t b = blockIdx.x;
-        const int cb = static_cast<int>(b % t.ncb);
-        const int64_t nk = b / t.ncb;
-        k = nk % t.K;
-        n = nk / t.K;
+        const uint32_t b = blockIdx.x;
+        const uint32_t nk = b / static_cast<uint32_t>(t.ncb);
+        const int cb = static_cast<int>(b - nk * static_cast<uint32_t>(t.ncb));
+        const uint32_t ns = nk / static_cast<uint32_t>(t.K);
+        k = nk - ns * static_cast<uint32_t>(t.K);
+        n = ns;
         r = static_cast<int>(threadIdx.x) / t.Pc;
-        const int pc = static_cast<int>(threadIdx.x) % t.Pc;
-        const int p = cb * t.Pc + pc;
+        const int p = cb * t.Pc + static_cast<int>(threadIdx.x) - r * t.Pc;
         active = r < t.R && p < t.P;
         c = active ? p * W : 0;
         lo = 0;
@@ -82,18 +85,63 @@ template <int W, bool TAIL> struct Place {
             lo = c + W - t.C;
             c = t.C - W;
         }
-        l = k * t.rpc;
-        l1 = l + t.rpc < t.L ? l + t.rpc : t.L;
-        l += r;
     }
 };
 
-// scale = gamma*rstd and shift = beta - mean*scale as the apply step folds
-// them, and the statistics, for a lane's W channels of sample n.
+// A workgroup's batches k, k + K, ...: the workgroups together move through
+// the sample as one front, and while a batch is worked on the next one's
+// loads are in flight.  `load` takes rows that exist (rows behind the last one
+// are read as the last one and not worked on).  BACK: from the sample's end.
+template <bool BACK, int U, class V> struct Stream {
+    const Tiles &tl;
+    int64_t r;
+    V a[U], b[U];
+    __device__ __forceinline__ Stream(const Tiles &t, int row_slot) : tl(t), r(row_slot) {}
+    __device__ __forceinline__ int64_t row(int64_t i, int u) const {
+        return ((BACK ? tl.batches - 1 - i : i) * U + u) * tl.R + r;
+    }
+    template <class Load>
+    __device__ __forceinline__ void fetch(V (&v)[U], int64_t i, Load &&load) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t l = row(i, u);
+            load(v[u], l < tl.L ? l : tl.L - 1);
+        }
+    }
+    template <class Work>
+    __device__ __forceinline__ void work(const V (&v)[U], int64_t i, Work &&w) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t l = row(i, u);
+            w(v[u], l, l < tl.L);
+        }
+    }
+    // The first batch's loads; before the loads of the channel parameters, so
+    // that their round trips overlap.
+    template <class Load> __device__ __forceinline__ void begin(int64_t k, Load &&load) {
+        fetch(a, k, load);
+    }
+    template <class Load, class Work>
+    __device__ __forceinline__ void run(int64_t k, Load &&load, Work &&w) {
+        for (int64_t i = k;;) {
+            int64_t n = i + tl.K;
+            if (n < tl.batches) fetch(b, n, load);
+            work(a, i, w);
+            if (n >= tl.batches) break;
+            i = n;
+            n += tl.K;
+            if (n < tl.batches) fetch(a, n, load);
+            work(b, i, w);
+            if (n >= tl.batches) break;
+            i = n;
+        }
+    }
+};
+
+// A lane's W channels of sample n: mean and rstd, scale = gamma*rstd, beta.
 template <int W> struct Channels {
-    float mu[W], rs[W], sc[W], sh[W];
+    float mu[W], rs[W], sc[W], be[W];
     __device__ __forceinline__ void load(const RowArgs &a, int64_t n, int c) {
-        float be[W];
         load_affine<W>(a.af.gamma, a.af.type, c, 1.0f, sc);
         load_affine<W>(a.af.beta, a.af.type, c, 0.0f, be);
 #pragma unroll
@@ -103,10 +151,7 @@ template <int W> struct Channels {
             rs[i] = a.rstd[g];
         }
 #pragma unroll
-        for (int i = 0; i < W; ++i) {
-            sc[i] *= rs[i];
-            sh[i] = fmaf(-mu[i], sc[i], be[i]);
-        }
+        for (int i = 0; i < W; ++i) sc[i] *= rs[i];
     }
 };
 
@@ -128,78 +173,68 @@ template <class D, int W, bool TAIL, bool SAVED> struct Pair {
             vx.template load<false>(static_cast<const T *>(a.x) + row * a.tl.C + c);
         vy.template load<false>(static_cast<const T *>(a.dy) + row * a.tl.C + c);
     }
-    __device__ __forceinline__ void x(int c, float (&o)[W]) const {
+    // x - mean: a saved value is widened and shifted in one fma
+    __device__ __forceinline__ void centred(int c, const float (&mu)[W], float (&o)[W]) const {
         if constexpr (SAVED) {
-            v8.widen(c, o);
+            v8.widen_less(c, mu, o);
         } else {
 #pragma unroll
-            for (int i = 0; i < W; ++i) o[i] = vx.get(i);
+            for (int i = 0; i < W; ++i) o[i] = vx.get(i) - mu[i];
         }
     }
 };
 
-// Pass 1.  U rows of a lane in flight.
-template <class D, int W, bool TAIL, bool SILU, bool SAVED, int U>
-__global__ __launch_bounds__(kLanes) void gn_grad_sums(RowArgs a) {
-    __shared__ float red[2 * W][kLanes];
+// Adds the tile's R row slots' values by a fixed tree, into slot 0.
+template <int W, int NT>
+__device__ __forceinline__ void slot_tree(float (&red)[W][NT], int r, const Tiles &tl,
+                                          float (&s)[W]) {
+    if (tl.R == 1) return;
+    int p2 = 1;
+    while (p2 < tl.R) p2 <<= 1;
+    __syncthreads();  // red is free
+#pragma unroll
+    for (int i = 0; i < W; ++i) red[i][threadIdx.x] = s[i];
+    for (int h = p2 >> 1; h > 0; h >>= 1) {
+        __syncthreads();
+        if (r < h && r + h < tl.R) {
+            const int o = static_cast<int>(threadIdx.x) + h * tl.Pc;
+#pragma unroll
+            for (int i = 0; i < W; ++i) red[i][threadIdx.x] = s[i] += red[i][o];
+        }
+    }
+}
+
+// Pass 1, by workgroups of NT lanes.
+template <class D, int W, bool TAIL, bool SILU, bool SAVED, int NT>
+__global__ __launch_bounds__(NT) void gn_grad_sums(RowArgs a) {
+    __shared__ float red[W][NT];
     const Tiles &tl = a.tl;
     const Place<W, TAIL> at(tl);
+    const int64_t nsb = (tl.C + kBlock8 - 1) / kBlock8;
+    const int64_t row0 = at.n * tl.L;
+    using V = Pair<D, W, TAIL, SAVED>;
+    auto load = [&](V &v, int64_t l) { v.load(a, row0 + l, nsb, at.c); };
+    Stream<false, kUnroll, V> st(tl, at.r);
+    st.begin(at.k, load);
     Channels<W> ch;
     ch.load(a, at.n, at.c);
     float s1[W], s2[W];
 #pragma unroll
     for (int i = 0; i < W; ++i) s1[i] = s2[i] = 0.0f;
-    const int64_t nsb = (tl.C + kBlock8 - 1) / kBlock8;
-    const int64_t row0 = at.n * tl.L;
-    using V = Pair<D, W, TAIL, SAVED>;
-    auto add = [&](const V &v) {
+    st.run(at.k, load, [&](const V &v, int64_t, bool live) {
+        if (!live) return;
         float x[W];
-        v.x(at.c, x);
+        v.centred(at.c, ch.mu, x);
 #pragma unroll
         for (int i = 0; i < W; ++i) {
             float d = v.vy.get(i);
-            if constexpr (SILU) d = silu_grad(fmaf(x[i], ch.sc[i], ch.sh[i]), d);
+            if constexpr (SILU) d = silu_grad(fmaf(x[i], ch.sc[i], ch.be[i]), d);
             s1[i] += d;
-            s2[i] = fmaf(d, x[i] - ch.mu[i], s2[i]);
+            s2[i] = fmaf(d, x[i], s2[i]);
         }
-    };
-    if (at.active) {
-        int64_t l = at.l;
-        for (; l + (U - 1) * int64_t{tl.R} < at.l1; l += U * int64_t{tl.R}) {
-            V v[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) v[u].load(a, row0 + l + u * int64_t{tl.R}, nsb, at.c);
-#pragma unroll
-            for (int u = 0; u < U; ++u) add(v[u]);
-        }
-        for (; l < at.l1; l += tl.R) {
-            V v;
-            v.load(a, row0 + l, nsb, at.c);
-            add(v);
-        }
-    }
-    // the R row slots, by a fixed tree
-    int p2 = 1;
-    while (p2 < tl.R) p2 <<= 1;
-    if (tl.R > 1) {
-#pragma unroll
-        for (int i = 0; i < W; ++i) {
-            red[i][threadIdx.x] = s1[i];
-            red[W + i][threadIdx.x] = s2[i];
-        }
-        __syncthreads();
-        for (int h = p2 >> 1; h > 0; h >>= 1) {
-            if (at.r < h && at.r + h < tl.R) {
-                const int o = static_cast<int>(threadIdx.x) + h * tl.Pc;
-#pragma unroll
-                for (int i = 0; i < W; ++i) {
-                    red[i][threadIdx.x] = s1[i] += red[i][o];
-                    red[W + i][threadIdx.x] = s2[i] += red[W + i][o];
-                }
-            }
-            __syncthreads();
-        }
-    }
+    });
+    slot_tree<W, NT>(red, at.r, tl, s1);
+    slot_tree<W, NT>(red, at.r, tl, s2);
     if (at.active && at.r == 0) {
         float *p = a.part + (at.n * tl.K + at.k) * 2 * tl.C + at.c;
 #pragma unroll
@@ -211,68 +246,97 @@ __global__ __launch_bounds__(kLanes) void gn_grad_sums(RowArgs a) {
     }
 }
 
-// Finishes pass 1: channel sums over the K chunks (16 parts of chunks per
-// workgroup, each in order, then the parts in order, in fp64), tile_c channels
-// of one sample per workgroup.  sums[N][2][C] receives sum dt and sum dt*h.
-// A tile of whole groups (Cg <= 64) also gives their a and b; one sample alone
-// its dgamma and dbeta.
-constexpr int kParts = 16;
+// Finishes pass 1: channel sums over the K partials, in fp64.  A workgroup
+// takes tile_c channels of one sample: its 1024 threads are 2^width lanes of
+// channels by 2^(10-width) parts of the partials, each part's partials added
+// in order, then the parts by fixed trees.  sums[N][2][C] receives sum dt and
+// sum dt*h.  A tile of whole groups (Cg <= 64) also gives their a and b; one
+// sample alone its dgamma and dbeta.  The narrowest tile that holds a group
+// (16 to 64 channels) has the most parts and so the shortest chain of loads.
+constexpr int kFinishThreads = 1024;
 struct FinishArgs {
     const float *part;
     const float *rstd;
     float *sums, *coef;
     void *dgamma, *dbeta;  // null unless N = 1 and wanted
     int64_t K;
-    int C, G, Cg, tile_c, tiles;
+    int C, G, Cg, tile_c, tiles, width;
     double inv_m;
     Affine af;
 };
-__global__ __launch_bounds__(64 * kParts) void gn_grad_finish(FinishArgs a) {
-    __shared__ double red[2][kParts][64];
-    const int lane = threadIdx.x & 63, r = threadIdx.x >> 6;
+__global__ __launch_bounds__(kFinishThreads) void gn_grad_finish(FinishArgs a) {
+    __shared__ double red[2][kFinishThreads / 64 * 64];
+    const int tid = threadIdx.x;
+    const int wide = 1 << a.width, parts = kFinishThreads >> a.width;
+    const int lane = tid & (wide - 1), r = tid >> a.width;
     const int64_t n = blockIdx.x / a.tiles;
     const int c = static_cast<int>(blockIdx.x % a.tiles) * a.tile_c + lane;
     const bool live = lane < a.tile_c && c < a.C;
     double s1 = 0.0, s2 = 0.0;
+    float ga[1] = {0.0f}, rs = 0.0f;
     if (live) {
+        // used at the end; their round trips overlap the partials'
+        rs = a.rstd[n * a.G + c / a.Cg];
+        load_affine<1>(a.af.gamma, a.af.type, c, 1.0f, ga);
         const float *p = a.part + n * a.K * 2 * a.C + c;
-#pragma unroll 4
-        for (int64_t k = r; k < a.K; k += kParts) {
-            s1 += static_cast<double>(p[k * 2 * a.C]);
-            s2 += static_cast<double>(p[k * 2 * a.C + a.C]);
+        // eight partials' loads in flight (the last ones clamped, not added)
+        constexpr int kBatch = 8;
+        const int64_t step = 2 * static_cast<int64_t>(a.C);
+        for (int64_t k = r; k < a.K; k += kBatch * parts) {
+            float v1[kBatch], v2[kBatch];
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                const int64_t ku = k + u * parts < a.K ? k + u * parts : a.K - 1;
+                v1[u] = p[ku * step];
+                v2[u] = p[ku * step + a.C];
+            }
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                const bool in = k + u * parts < a.K;
+                s1 += in ? static_cast<double>(v1[u]) : 0.0;
+                s2 += in ? static_cast<double>(v2[u]) : 0.0;
+            }
         }
     }
-    red[0][r][lane] = s1;
-    red[1][r][lane] = s2;
-    __syncthreads();
-    if (r != 0) return;
-#pragma unroll
-    for (int i = 1; i < kParts; ++i) {
-        s1 += red[0][i][lane];
-        s2 += red[1][i][lane];
+    // the parts within a wave by a butterfly, then the 16 waves' sums: wave 0
+    // adds each channel's in `per` interleaved runs and joins those
+    const int per = 64 >> a.width;
+    for (int o = wide; o < 64; o <<= 1) {
+        s1 += __shfl_xor(s1, o, 64);
+        s2 += __shfl_xor(s2, o, 64);
     }
-    float ga[1] = {0.0f};
-    if (live) {
-        s2 *= static_cast<double>(a.rstd[n * a.G + c / a.Cg]);
+    if ((tid & 63) < wide) {
+        red[0][(tid >> 6) * wide + lane] = s1;
+        red[1][(tid >> 6) * wide + lane] = s2;
+    }
+    __syncthreads();
+    if (tid >= 64) return;
+    s1 = s2 = 0.0;
+#pragma unroll 4
+    for (int w = r; w < kFinishThreads / 64; w += per) {
+        s1 += red[0][w * wide + lane];
+        s2 += red[1][w * wide + lane];
+    }
+    for (int o = wide; o < 64; o <<= 1) {
+        s1 += __shfl_xor(s1, o, 64);
+        s2 += __shfl_xor(s2, o, 64);
+    }
+    s2 *= static_cast<double>(rs);
+    if (live && r == 0) {
         a.sums[n * 2 * a.C + c] = static_cast<float>(s1);
         a.sums[n * 2 * a.C + a.C + c] = static_cast<float>(s2);
         if (a.dbeta != nullptr) store_affine(a.dbeta, a.af.type, c, static_cast<float>(s1));
         if (a.dgamma != nullptr) store_affine(a.dgamma, a.af.type, c, static_cast<float>(s2));
-        load_affine<1>(a.af.gamma, a.af.type, c, 1.0f, ga);
     }
     if (a.coef == nullptr) return;
-    // one wave is left: its LDS accesses are in order
-    red[0][0][lane] = s1 * static_cast<double>(ga[0]);
-    red[1][0][lane] = s2 * static_cast<double>(ga[0]);
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");
-    if (live && lane % a.Cg == 0) {
-        double ta = 0.0, tb = 0.0;
-        for (int i = 0; i < a.Cg; ++i) {
-            ta += red[0][0][lane + i];
-            tb += red[1][0][lane + i];
-        }
+    s1 *= static_cast<double>(ga[0]);
+    s2 *= static_cast<double>(ga[0]);
+    double ta = 0.0, tb = 0.0;
+    for (int i = 0; i < a.Cg; ++i) {  // lanes lane .. lane + Cg - 1: the lane's group
+        ta += __shfl(s1, lane + i, 64);
+        tb += __shfl(s2, lane + i, 64);
+    }
+    if (live && r == 0 && lane % a.Cg == 0) {
         float *o = a.coef + 2 * (n * a.G + c / a.Cg);
         o[0] = static_cast<float>(ta * a.inv_m);
         o[1] = static_cast<float>(tb * a.inv_m);
@@ -324,13 +388,21 @@ __global__ __launch_bounds__(kLanes) void gn_grad_samples(const float *sums, int
     if (dgamma != nullptr) store_affine(dgamma, type, c, static_cast<float>(s2));
 }
 
-// Pass 2: dx = dt*scale - (x-mean)*rstd^2*b - rstd*a.
-template <class D, int W, bool TAIL, bool SILU, bool SAVED, int U>
+// Pass 2: dx = dt*scale - (x-mean)*rstd^2*b - rstd*a, from the rows that pass 1
+// read last to those that it read first, so that what the Infinity Cache still
+// holds of x and dy is read before it is replaced; dx is stored nontemporally
+// for the same reason.
+template <class D, int W, bool TAIL, bool SILU, bool SAVED>
 __global__ __launch_bounds__(kLanes) void gn_grad_input(RowArgs a) {
     using T = typename D::storage;
     const Tiles &tl = a.tl;
     const Place<W, TAIL> at(tl);
-    if (!at.active) return;
+    const int64_t nsb = (tl.C + kBlock8 - 1) / kBlock8;
+    const int64_t row0 = at.n * tl.L;
+    using V = Pair<D, W, TAIL, SAVED>;
+    auto load = [&](V &v, int64_t l) { v.load(a, row0 + l, nsb, at.c); };
+    Stream<true, SAVED ? kUnroll : kInputUnroll, V> st(tl, at.r);
+    st.begin(at.k, load);
     Channels<W> ch;
     ch.load(a, at.n, at.c);
     float k0[W], k1[W];
@@ -340,152 +412,124 @@ __global__ __launch_bounds__(kLanes) void gn_grad_input(RowArgs a) {
         k0[i] = -ch.rs[i] * co[0];
         k1[i] = -ch.rs[i] * ch.rs[i] * co[1];
     }
-    const int64_t nsb = (tl.C + kBlock8 - 1) / kBlock8;
-    const int64_t row0 = at.n * tl.L;
-    using V = Pair<D, W, TAIL, SAVED>;
-    auto finish = [&](const V &v, int64_t row) {
+    st.run(at.k, load, [&](const V &v, int64_t l, bool live) {
+        if (!live || !at.active) return;
         float x[W], o[W];
-        v.x(at.c, x);
+        v.centred(at.c, ch.mu, x);
 #pragma unroll
         for (int i = 0; i < W; ++i) {
             float d = v.vy.get(i);
-            if constexpr (SILU) d = silu_grad(fmaf(x[i], ch.sc[i], ch.sh[i]), d);
-            o[i] = fmaf(d, ch.sc[i], fmaf(x[i] - ch.mu[i], k1[i], k0[i]));
+            if constexpr (SILU) d = silu_grad(fmaf(x[i], ch.sc[i], ch.be[i]), d);
+            o[i] = fmaf(d, ch.sc[i], fmaf(x[i], k1[i], k0[i]));
         }
-        T *p = static_cast<T *>(a.y) + row * tl.C + at.c;
+        T *p = static_cast<T *>(a.y) + (row0 + l) * tl.C + at.c;
         // dx may be dy or x: a lane writes only channels that no other reads
         if (!TAIL || at.lo == 0)
-            Piece<D, W>::template store<false>(p, o);
+            Piece<D, W>::template store<true>(p, o);
         else
             store_from<D, W>(p, o, at.lo);
-    };
-    int64_t l = at.l;
-    for (; l + (U - 1) * int64_t{tl.R} < at.l1; l += U * int64_t{tl.R}) {
-        V v[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) v[u].load(a, row0 + l + u * int64_t{tl.R}, nsb, at.c);
-#pragma unroll
-        for (int u = 0; u < U; ++u) finish(v[u], row0 + l + u * int64_t{tl.R});
-    }
-    for (; l < at.l1; l += tl.R) {
-        V v;
-        v.load(a, row0 + l, nsb, at.c);
-        finish(v, row0 + l);
-    }
+    });
 }
 
 // The apply step that also saves x (kApply, kApplySilu), or x saved alone
 // (kSave).  A block of the format lies in consecutive lanes of one row: the
 // plan makes Pc a multiple of the lanes that hold a block.
 enum { kApply = 0, kApplySilu = 1, kSave = 2 };
-template <class D, int W, bool TAIL, int MODE, int U>
+template <class D, int W, bool TAIL, int MODE>
 __global__ __launch_bounds__(kLanes) void gn_rows_save(RowArgs a) {
     using T = typename D::storage;
     constexpr int kGroup = W == 1 ? 8 : kBlock8 / W;
     const Tiles &tl = a.tl;
     const Place<W, TAIL> at(tl);
-    Channels<W> ch;
-    if constexpr (MODE != kSave) ch.load(a, at.n, at.c);
     const int64_t nsb = (tl.C + kBlock8 - 1) / kBlock8;
     const int64_t row0 = at.n * tl.L;
-    const int lo = at.active ? at.lo : W;
-    // every lane of the workgroup takes part in the blocks' maxima
-    for (int64_t l = at.l - at.r; l < at.l1; l += U * int64_t{tl.R}) {
-        Piece<D, W> v[U];
-        int64_t row[U];
-        bool live[U];
+    using V = Piece<D, W>;
+    auto load = [&](V &v, int64_t l) {
+        v.template load<false>(static_cast<const T *>(a.x) + (row0 + l) * a.x_stride + at.c);
+    };
+    Stream<false, kUnroll, V> st(tl, at.r);
+    st.begin(at.k, load);
+    float sc[W], sh[W];
+    if constexpr (MODE != kSave) {  // scale and shift as the apply step folds them
+        Channels<W> ch;
+        ch.load(a, at.n, at.c);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t lu = l + at.r + u * int64_t{tl.R};
-            live[u] = at.active && lu < at.l1;
-            row[u] = row0 + (live[u] ? lu : at.l1 - 1);
-            v[u].template load<false>(static_cast<const T *>(a.x) + row[u] * a.x_stride + at.c);
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            float x[W];
-#pragma unroll
-            for (int i = 0; i < W; ++i) x[i] = v[u].get(i);
-            if constexpr (MODE != kSave) {
-                float o[W];
-#pragma unroll
-                for (int i = 0; i < W; ++i) {
-                    const float t = fmaf(x[i], ch.sc[i], ch.sh[i]);
-                    o[i] = MODE == kApplySilu ? silu_f32(t) : t;
-                }
-                T *p = static_cast<T *>(a.y) + row[u] * a.y_stride + at.c;
-                if (live[u]) {  // y may be x: only the lane's own channels
-                    if (!TAIL || at.lo == 0)
-                        Piece<D, W>::template store<false>(p, o);
-                    else
-                        store_from<D, W>(p, o, at.lo);
-                }
-            }
-            const uint32_t E = block8_exponent<W, kGroup>(x, lo);
-            const Codes<W> q = block8_encode<W>(x, E);
-            if (live[u])
-                store_block8<W, TAIL>(q, E, a.codes_out, a.scales_out, row[u] * tl.C,
-                                      row[u] * nsb, at.c, at.lo);
+        for (int i = 0; i < W; ++i) {
+            sc[i] = ch.sc[i];
+            sh[i] = fmaf(-ch.mu[i], ch.sc[i], ch.be[i]);
         }
     }
+    const Magnitudes<D, W> mag(at.active ? at.lo : W);
+    // every lane of the workgroup takes part in the blocks' maxima
+    st.run(at.k, load, [&](const V &v, int64_t l, bool live) {
+        const int64_t row = row0 + l;
+        float x[W];
+#pragma unroll
+        for (int i = 0; i < W; ++i) x[i] = v.get(i);
+        const uint32_t E = block8_exponent<D, W, kGroup>(v, mag);
+        if (!live || !at.active) return;
+        if constexpr (MODE != kSave) {
+            float o[W];
+#pragma unroll
+            for (int i = 0; i < W; ++i) {
+                const float t = fmaf(x[i], sc[i], sh[i]);
+                o[i] = MODE == kApplySilu ? silu_f32(t) : t;
+            }
+            T *p = static_cast<T *>(a.y) + row * a.y_stride + at.c;
+            if (!TAIL || at.lo == 0)  // y may be x: only the lane's own channels
+                Piece<D, W>::template store<true>(p, o);
+            else
+                store_from<D, W>(p, o, at.lo);
+        }
+        store_block8<W, TAIL, true>(block8_encode<W>(x, E), E, a.codes_out, a.scales_out,
+                                    row * tl.C, row * nsb, at.c, at.lo);
+    });
 }
 
 // Saved rows widened again.
-template <class D, int W, bool TAIL, int U>
+template <class D, int W, bool TAIL>
 __global__ __launch_bounds__(kLanes) void gn_rows_restore(RowArgs a) {
     using T = typename D::storage;
     const Tiles &tl = a.tl;
     const Place<W, TAIL> at(tl);
-    if (!at.active) return;
     const int64_t nsb = (tl.C + kBlock8 - 1) / kBlock8;
     const int64_t row0 = at.n * tl.L;
-    auto put = [&](const Piece8<W, TAIL> &v, int64_t row) {
+    using V = Piece8<W, TAIL>;
+    auto load = [&](V &v, int64_t l) {
+        v.load(a.codes, a.scales, (row0 + l) * tl.C, (row0 + l) * nsb, at.c);
+    };
+    Stream<false, kUnroll, V> st(tl, at.r);
+    st.begin(at.k, load);
+    st.run(at.k, load, [&](const V &v, int64_t l, bool live) {
+        if (!live || !at.active) return;
         float o[W];
         v.widen(at.c, o);
-        Piece<D, W>::template store<false>(static_cast<T *>(a.y) + row * a.y_stride + at.c, o);
-    };
-    int64_t l = at.l;
-    for (; l + (U - 1) * int64_t{tl.R} < at.l1; l += U * int64_t{tl.R}) {
-        Piece8<W, TAIL> v[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t row = row0 + l + u * int64_t{tl.R};
-            v[u].load(a.codes, a.scales, row * tl.C, row * nsb, at.c);
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) put(v[u], row0 + l + u * int64_t{tl.R});
-    }
-    for (; l < at.l1; l += tl.R) {
-        Piece8<W, TAIL> v;
-        const int64_t row = row0 + l;
-        v.load(a.codes, a.scales, row * tl.C, row * nsb, at.c);
-        put(v, row);
-    }
+        Piece<D, W>::template store<true>(
+            static_cast<T *>(a.y) + (row0 + l) * a.y_stride + at.c, o);
+    });
 }
 
 // ---- host -----------------------------------------------------------------------
-constexpr int kUnroll = 4;                  // rows of a lane in flight
-constexpr int64_t kSumBlocks = 512;         // pass 1: workgroups, 2 per CU
+constexpr int64_t kSumBlocks = 512;         // pass 1: workgroups of kSumLanes, 1 per CU
 constexpr int64_t kStreamBlocks = 2048;     // the other passes
+constexpr int64_t kSmallBytes = int64_t{16} << 20;  // x at most this: latency rules
 constexpr int64_t kMaxRun = 1024;           // rows a lane adds up in fp32
 
 // whole: lanes that must stay in one row together (a block of the format when
 // saving, else 1).
 Tiles make_tiles(int64_t N, int64_t L, int64_t C, int w, int whole, int64_t blocks,
-                 int64_t max_run) {
+                 int64_t max_run = 0, int lanes = kLanes, int unroll = kUnroll) {
     Tiles t{};
     t.L = L;
     t.C = static_cast<int>(C);
     t.P = static_cast<int>(ceil_div(C, w));
-    t.ncb = static_cast<int>(ceil_div(t.P, kLanes));
+    t.ncb = static_cast<int>(ceil_div(t.P, lanes));
     t.Pc = static_cast<int>(ceil_div(ceil_div(t.P, t.ncb), whole)) * whole;
-    t.R = kLanes / t.Pc;
-    const int64_t tiles = std::max<int64_t>(1, ceil_div(L, t.R));
+    t.R = lanes / t.Pc;
+    t.batches = std::max<int64_t>(1, ceil_div(L, int64_t{t.R} * unroll));
     int64_t k = std::max<int64_t>(1, blocks / std::max<int64_t>(1, N * t.ncb));
-    k = std::min(k, ceil_div(tiles, kUnroll));
-    if (max_run > 0) k = std::max(k, ceil_div(tiles, max_run));
-    t.rpc = ceil_div(tiles, k) * t.R;
-    t.K = std::max<int64_t>(1, ceil_div(L, t.rpc));
+    if (max_run > 0) k = std::max(k, ceil_div(t.batches * unroll, max_run));
+    t.K = std::min(k, t.batches);
     return t;
 }
 
@@ -521,9 +565,9 @@ dim3 grid_of(int64_t N, const Tiles &t) {
     return dim3(static_cast<unsigned>(N * t.K * t.ncb));
 }
 // A dispatch holds fewer than 2^32 work-items.
-bool grid_fits(int64_t N, const Tiles &t) {
-    return N < (int64_t{1} << 24) && t.K < (int64_t{1} << 24) &&
-           N * t.K < (int64_t{1} << 24) && N * t.K * t.ncb < (int64_t{1} << 24);
+bool grid_fits(int64_t N, const Tiles &t, int lanes = kLanes) {
+    const int64_t most = (int64_t{1} << 32) / lanes;
+    return N < most && t.K < most && N * t.K < most && N * t.K * t.ncb < most;
 }
 
 bool misaligned(const void *p, int64_t bytes) {
@@ -543,23 +587,28 @@ gn_status check_group_rows(int64_t N, int64_t L, int64_t C, int64_t G, int apply
 
 struct BackwardPlan {
     Tiles sums, input;
-    int tile_c, tiles;
+    int lanes;  // of pass 1's workgroups
+    int tile_c, tiles, width;
     size_t part, total;  // floats
 };
-BackwardPlan backward_plan(int64_t N, int64_t L, int64_t C, int64_t G, int dtype) {
+BackwardPlan backward_plan(int64_t N, int64_t L, int64_t C, int64_t G, int dtype, bool saved) {
     BackwardPlan p;
     const int w = piece_width(C, dtype);
-    p.sums = make_tiles(N, L, C, w, 1, kSumBlocks, kMaxRun);
-    p.input = make_tiles(N, L, C, w, 1, kStreamBlocks, 0);
+    p.lanes = N * L * C * elem_bytes(dtype) <= kSmallBytes ? kLanes : kSumLanes;
+    p.sums = make_tiles(N, L, C, w, 1, kSumBlocks, kMaxRun, p.lanes);
+    p.input = make_tiles(N, L, C, w, 1, kStreamBlocks, 0, kLanes,
+                         saved ? kUnroll : kInputUnroll);
     const int64_t cg = C / G;
-    p.tile_c = static_cast<int>(cg <= 64 ? 64 / cg * cg : 64);
+    p.width = cg <= 16 || cg > 64 ? 4 : (cg <= 32 ? 5 : 6);
+    const int64_t wide = int64_t{1} << p.width;
+    p.tile_c = static_cast<int>(cg <= 64 ? wide / cg * cg : wide);
     p.tiles = static_cast<int>(ceil_div(C, p.tile_c));
     p.part = static_cast<size_t>(N) * p.sums.K * 2 * C;
     p.total = p.part + static_cast<size_t>(N) * 2 * (C + G);
     return p;
 }
 bool backward_fits(int64_t N, const BackwardPlan &p) {
-    return grid_fits(N, p.sums) && grid_fits(N, p.input) && N * p.tiles < (int64_t{1} << 22) &&
+    return grid_fits(N, p.sums, p.lanes) && grid_fits(N, p.input) && N * p.tiles < (int64_t{1} << 22) &&
            N * p.sums.C < (int64_t{1} << 40);
 }
 
@@ -591,7 +640,7 @@ gn_status gn_checkpoint_rows(const void *x, int64_t x_stride, void *codes, void 
     if (M == 0) return GN_OK;
     const int w = piece_width(C, dtype);
     RowArgs a{};
-    a.tl = make_tiles(1, M, C, w, block_lanes(w), kStreamBlocks, 0);
+    a.tl = make_tiles(1, M, C, w, block_lanes(w), kStreamBlocks);
     if (!grid_fits(1, a.tl)) return GN_UNSUPPORTED;
     Call c;
     st = begin_call(stream, {x, codes, scales}, &c);
@@ -601,7 +650,7 @@ gn_status gn_checkpoint_rows(const void *x, int64_t x_stride, void *codes, void 
     a.scales_out = static_cast<uint8_t *>(scales);
     a.x_stride = x_stride;
     with_pieces(C, dtype, [&](auto d, auto wc, auto tail) {
-        gn_rows_save<decltype(d), decltype(wc)::value, decltype(tail)::value != 0, kSave, kUnroll>
+        gn_rows_save<decltype(d), decltype(wc)::value, decltype(tail)::value != 0, kSave>
             <<<grid_of(1, a.tl), kLanes, 0, c.stream>>>(a);
     });
     return finish_launch();
@@ -616,7 +665,7 @@ gn_status gn_restore_rows(const void *codes, const void *scales, void *x, int64_
     if (M == 0) return GN_OK;
     const int w = piece_width(C, dtype);
     RowArgs a{};
-    a.tl = make_tiles(1, M, C, w, 1, kStreamBlocks, 0);
+    a.tl = make_tiles(1, M, C, w, 1, kStreamBlocks);
     if (!grid_fits(1, a.tl)) return GN_UNSUPPORTED;
     Call c;
     st = begin_call(stream, {x, codes, scales}, &c);
@@ -626,7 +675,7 @@ gn_status gn_restore_rows(const void *codes, const void *scales, void *x, int64_
     a.y = x;
     a.y_stride = x_stride;
     with_pieces(C, dtype, [&](auto d, auto wc, auto tail) {
-        gn_rows_restore<decltype(d), decltype(wc)::value, decltype(tail)::value != 0, kUnroll>
+        gn_rows_restore<decltype(d), decltype(wc)::value, decltype(tail)::value != 0>
             <<<grid_of(1, a.tl), kLanes, 0, c.stream>>>(a);
     });
     return finish_launch();
@@ -648,7 +697,7 @@ gn_status gn_apply_rows_save(const void *x, const float *mean, const float *rstd
     if (N * L == 0) return GN_OK;
     const int w = piece_width(C, dtype);
     RowArgs a{};
-    a.tl = make_tiles(N, L, C, w, block_lanes(w), kStreamBlocks, 0);
+    a.tl = make_tiles(N, L, C, w, block_lanes(w), kStreamBlocks);
     if (!grid_fits(N, a.tl)) return GN_UNSUPPORTED;
     Call c;
     st = begin_call(stream, {x, mean, rstd, gamma, beta, y, codes, scales}, &c);
@@ -668,10 +717,10 @@ gn_status gn_apply_rows_save(const void *x, const float *mean, const float *rstd
         constexpr int W = decltype(wc)::value;
         constexpr bool TAIL = decltype(tail)::value != 0;
         if (apply_silu)
-            gn_rows_save<D, W, TAIL, kApplySilu, kUnroll>
+            gn_rows_save<D, W, TAIL, kApplySilu>
                 <<<grid_of(N, a.tl), kLanes, 0, c.stream>>>(a);
         else
-            gn_rows_save<D, W, TAIL, kApply, kUnroll>
+            gn_rows_save<D, W, TAIL, kApply>
                 <<<grid_of(N, a.tl), kLanes, 0, c.stream>>>(a);
     });
     return finish_launch();
@@ -686,7 +735,7 @@ gn_status gn_silu_rows_backward_workspace(int64_t N, int64_t L, int64_t C, int64
         *bytes_out = 0;
         return GN_OK;
     }
-    const BackwardPlan p = backward_plan(N, L, C, G, dtype);
+    const BackwardPlan p = backward_plan(N, L, C, G, dtype, false);
     if (!backward_fits(N, p)) return GN_UNSUPPORTED;
     *bytes_out = static_cast<int64_t>(sizeof(float) * p.total);
     return GN_OK;
@@ -716,7 +765,7 @@ gn_status gn_silu_rows_backward(const void *dy, const void *x, const void *codes
     if (empty && !grads) return GN_OK;
     BackwardPlan p{};
     if (!empty) {
-        p = backward_plan(N, L, C, G, dtype);
+        p = backward_plan(N, L, C, G, dtype, codes != nullptr);
         if (!backward_fits(N, p)) return GN_UNSUPPORTED;
         if (workspace == nullptr) return GN_INVALID_ARGUMENT;
         if (workspace_bytes < 0 || static_cast<size_t>(workspace_bytes) < sizeof(float) * p.total)
@@ -761,6 +810,7 @@ gn_status gn_silu_rows_backward(const void *dy, const void *x, const void *codes
     f.Cg = a.Cg;
     f.tile_c = p.tile_c;
     f.tiles = p.tiles;
+    f.width = p.width;
     f.inv_m = 1.0 / (static_cast<double>(L) * static_cast<double>(a.Cg));
     f.af = a.af;
     f.coef = a.Cg <= 64 ? coef : nullptr;
@@ -773,9 +823,13 @@ gn_status gn_silu_rows_backward(const void *dy, const void *x, const void *codes
             constexpr bool SILU = decltype(silu)::value != 0;
             constexpr bool SAVED = decltype(saved)::value != 0;
             a.tl = p.sums;
-            gn_grad_sums<D, W, TAIL, SILU, SAVED, kUnroll>
-                <<<grid_of(N, a.tl), kLanes, 0, c.stream>>>(a);
-            gn_grad_finish<<<dim3(static_cast<unsigned>(N * p.tiles)), 64 * kParts, 0, c.stream>>>(
+            if (p.lanes == kLanes)
+                gn_grad_sums<D, W, TAIL, SILU, SAVED, kLanes>
+                    <<<grid_of(N, a.tl), kLanes, 0, c.stream>>>(a);
+            else
+                gn_grad_sums<D, W, TAIL, SILU, SAVED, kSumLanes>
+                    <<<grid_of(N, a.tl), kSumLanes, 0, c.stream>>>(a);
+            gn_grad_finish<<<dim3(static_cast<unsigned>(N * p.tiles)), kFinishThreads, 0, c.stream>>>(
                 f);
             if (f.coef == nullptr) {
                 FinishArgs g = f;
@@ -783,7 +837,7 @@ gn_status gn_silu_rows_backward(const void *dy, const void *x, const void *codes
                 gn_grad_groups<<<dim3(static_cast<unsigned>(N * G)), kLanes, 0, c.stream>>>(g);
             }
             a.tl = p.input;
-            gn_grad_input<D, W, TAIL, SILU, SAVED, kUnroll>
+            gn_grad_input<D, W, TAIL, SILU, SAVED>
                 <<<grid_of(N, a.tl), kLanes, 0, c.stream>>>(a);
         };
         auto by_saved = [&](auto silu) {

@@ -154,10 +154,10 @@ __global__ __launch_bounds__(THREADS) void gn_layer_norm(LnArgs a) {
             // writes, computed alike.
             if (live && lo[j] < W) Piece<D, W>::template store<false>(y + m * a.y_stride + c[j], o);
             if constexpr (SAVE) {
-                const uint32_t E = block8_exponent<W, kGroup>(f, lo[j]);
+                const uint32_t E = block8_exponent<D, W, kGroup>(v[j], Magnitudes<D, W>(lo[j]));
                 const Codes<W> qd = block8_encode<W>(f, E);
                 if (live && lo[j] < W)
-                    store_block8<W, TAIL>(qd, E, a.codes_out, a.scales_out, m * a.C, m * nsb,
+                    store_block8<W, TAIL, false>(qd, E, a.codes_out, a.scales_out, m * a.C, m * nsb,
                                           c[j], lo[j]);
             }
         }

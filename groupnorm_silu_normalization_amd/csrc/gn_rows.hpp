@@ -16,6 +16,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "gn_types.hpp"
 
 namespace gnsilu {
@@ -209,9 +211,11 @@ __device__ __forceinline__ uint32_t lane_max(uint32_t v) {
 // has E = 255 and stands for NaN throughout.
 constexpr int kBlock8 = 32;
 
-__device__ __forceinline__ float block8_step(uint32_t E) {  // 2^(E - 133)
-    return E == 255u ? __uint_as_float(0x7fc00000u)
-                     : __builtin_ldexpf(1.0f, static_cast<int>(E) - 133);
+// 2^(E - 133); NaN for E = 255, by bits: a select of the NaN would be moved
+// behind every product with the step.
+__device__ __forceinline__ float block8_step(uint32_t E) {
+    const float s = __builtin_ldexpf(1.0f, static_cast<int>(E) - 133);
+    return __uint_as_float(__float_as_uint(s) | (E == 255u ? 0x7fc00000u : 0u));
 }
 
 template <int W> struct Codes;  // a piece's W codes, one byte each
@@ -220,8 +224,11 @@ template <> struct Codes<8> {
     __device__ __forceinline__ void load(const int8_t *p) {
         w = *reinterpret_cast<const u32x2_a1 *>(p);
     }
-    __device__ __forceinline__ void store(int8_t *p) const {
-        *reinterpret_cast<u32x2_a1 *>(p) = w;
+    template <bool NT> __device__ __forceinline__ void store(int8_t *p) const {
+        if constexpr (NT)
+            __builtin_nontemporal_store(w, reinterpret_cast<u32x2_a1 *>(p));
+        else
+            *reinterpret_cast<u32x2_a1 *>(p) = w;
     }
     __device__ __forceinline__ int get(int j) const {
         return static_cast<int8_t>(w[j >> 2] >> (8 * (j & 3)));
@@ -233,8 +240,11 @@ template <> struct Codes<4> {
     __device__ __forceinline__ void load(const int8_t *p) {
         w = *reinterpret_cast<const u32_a1 *>(p);
     }
-    __device__ __forceinline__ void store(int8_t *p) const {
-        *reinterpret_cast<u32_a1 *>(p) = w;
+    template <bool NT> __device__ __forceinline__ void store(int8_t *p) const {
+        if constexpr (NT)
+            __builtin_nontemporal_store(w, reinterpret_cast<u32_a1 *>(p));
+        else
+            *reinterpret_cast<u32_a1 *>(p) = w;
     }
     __device__ __forceinline__ int get(int j) const { return static_cast<int8_t>(w >> (8 * j)); }
     __device__ __forceinline__ void set4(int, uint32_t v) { w = v; }
@@ -242,7 +252,9 @@ template <> struct Codes<4> {
 template <> struct Codes<1> {
     uint32_t w;
     __device__ __forceinline__ void load(const int8_t *p) { w = static_cast<uint8_t>(*p); }
-    __device__ __forceinline__ void store(int8_t *p) const { *p = static_cast<int8_t>(w); }
+    template <bool NT> __device__ __forceinline__ void store(int8_t *p) const {
+        *p = static_cast<int8_t>(w);
+    }
     __device__ __forceinline__ int get(int) const { return static_cast<int8_t>(w); }
 };
 
@@ -271,20 +283,76 @@ template <int W, bool TAIL> struct Piece8 {
             for (int j = 0; j < W; ++j) o[j] = static_cast<float>(q.get(j)) * s0;
         }
     }
+    // The values less mu, in one fma each.
+    __device__ __forceinline__ void widen_less(int c, const float (&mu)[W], float (&o)[W]) const {
+        const float s0 = block8_step(e0);
+        const float s1 = TAIL ? block8_step(e1) : 0.0f;
+        const int split = TAIL ? kBlock8 - c % kBlock8 : W;
+#pragma unroll
+        for (int j = 0; j < W; ++j)
+            o[j] = fmaf(static_cast<float>(q.get(j)), TAIL && j >= split ? s1 : s0, -mu[j]);
+    }
 };
+
+// Which bits of a raw piece count for its block's maximum: the magnitudes of
+// the channels j >= lo.  Cleared words cost nothing, as the signs have to be
+// masked off anyway.
+template <class D, int W> struct Magnitudes {
+    static constexpr bool k16 = sizeof(typename D::storage) == 2;
+    static constexpr int kWords = W == 8 ? 4 : W;
+    uint32_t m[kWords];
+    __device__ __forceinline__ explicit Magnitudes(int lo) {
+#pragma unroll
+        for (int k = 0; k < kWords; ++k) {
+            if constexpr (k16 && W == 8)
+                m[k] = (2 * k >= lo ? 0x7fffu : 0u) | (2 * k + 1 >= lo ? 0x7fff0000u : 0u);
+            else if constexpr (k16)
+                m[k] = k >= lo ? 0x7fffu : 0u;
+            else
+                m[k] = k >= lo ? 0x7fffffffu : 0u;
+        }
+    }
+};
+
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t max2_u16(uint32_t a, uint32_t b) {
+    return __builtin_bit_cast(uint32_t,
+                              __builtin_elementwise_max(__builtin_bit_cast(u16x2, a),
+                                                        __builtin_bit_cast(u16x2, b)));
+}
 
 // The scale byte of the block that the calling lane's piece belongs to; the
 // block's pieces are held by GROUP consecutive, aligned lanes (all of which
-// call this).  Channels j < lo are another piece's and do not count.
-template <int W, int GROUP>
-__device__ __forceinline__ uint32_t block8_exponent(const float (&v)[W], int lo) {
-    uint32_t top = 0;
+// call this).  Magnitudes of every type order like their bits, so the maxima
+// are taken on the raw words, two 16-bit values at a time.
+template <class D, int W, int GROUP>
+__device__ __forceinline__ uint32_t block8_exponent(const Piece<D, W> &v,
+                                                    const Magnitudes<D, W> &mag) {
+    uint32_t top;
+    if constexpr (W == 8) {
+        top = max2_u16(max2_u16(v.w[0] & mag.m[0], v.w[1] & mag.m[1]),
+                       max2_u16(v.w[2] & mag.m[2], v.w[3] & mag.m[3]));
+        const uint32_t hi = top >> 16, lo = top & 0xffffu;
+        top = hi > lo ? hi : lo;
+    } else if constexpr (W == 4) {
+        top = v.w[0] & mag.m[0];
 #pragma unroll
-    for (int j = 0; j < W; ++j) {
-        const uint32_t b = __float_as_uint(v[j]) & 0x7fffffffu;
-        top = (j >= lo && b > top) ? b : top;
+        for (int k = 1; k < 4; ++k) {
+            const uint32_t b = v.w[k] & mag.m[k];
+            top = b > top ? b : top;
+        }
+    } else if constexpr (sizeof(v.b) == 2) {
+        top = v.b & mag.m[0];
+    } else {
+        top = __float_as_uint(v.b) & mag.m[0];
     }
-    return lane_max<GROUP>(top) >> 23;
+    top = lane_max<GROUP>(top);
+    if constexpr (std::is_same<D, Bf16>::value)
+        return top >> 7;
+    else if constexpr (std::is_same<D, Fp16>::value)
+        return __float_as_uint(Fp16::to_f32(static_cast<uint16_t>(top))) >> 23;
+    else
+        return top >> 23;
 }
 
 // rint by adding 1.5 * 2^23: the sum's low byte is the code in two's
@@ -292,32 +360,37 @@ __device__ __forceinline__ uint32_t block8_exponent(const float (&v)[W], int lo)
 template <int W>
 __device__ __forceinline__ Codes<W> block8_encode(const float (&v)[W], uint32_t E) {
     uint32_t b[W];
+    const int e = 133 - static_cast<int>(E);
 #pragma unroll
     for (int j = 0; j < W; ++j) {
-        const float t = __builtin_ldexpf(v[j], 133 - static_cast<int>(E));
-        b[j] = __float_as_uint(__builtin_amdgcn_fmed3f(t, -127.0f, 127.0f) + 12582912.0f) & 0xffu;
-        if (E == 255u) b[j] = 0u;
+        const float t = __builtin_ldexpf(v[j], e);
+        b[j] = __float_as_uint(__builtin_amdgcn_fmed3f(t, -127.0f, 127.0f) + 12582912.0f);
     }
+    const uint32_t keep = E == 255u ? 0u : ~0u;
     Codes<W> q;
     if constexpr (W == 1) {
-        q.w = b[0];
+        q.w = b[0] & keep;
     } else {
+        // v_perm_b32: selector bytes 0-3 take the second operand's bytes, 4-7
+        // the first's, 12 zero
 #pragma unroll
         for (int k = 0; k < W / 4; ++k)
-            q.set4(k, b[4 * k] | (b[4 * k + 1] << 8) | (b[4 * k + 2] << 16) | (b[4 * k + 3] << 24));
+            q.set4(k, (__builtin_amdgcn_perm(b[4 * k + 1], b[4 * k], 0x0c0c0400u) |
+                       __builtin_amdgcn_perm(b[4 * k + 3], b[4 * k + 2], 0x04000c0cu)) &
+                          keep);
     }
     return q;
 }
 
 // Writes a piece's codes and, from the block's first piece, its scale.
 // c: the piece's first channel in memory; lo: its first own channel.
-template <int W, bool TAIL>
+template <int W, bool TAIL, bool NT>
 __device__ __forceinline__ void store_block8(const Codes<W> &q, uint32_t E, int8_t *codes,
                                              uint8_t *scales, int64_t row_c, int64_t row_s, int c,
                                              int lo) {
     int8_t *p = codes + row_c + c;
     if (!TAIL || lo == 0) {
-        q.store(p);
+        q.template store<NT>(p);
     } else {
 #pragma unroll
         for (int j = 0; j < W; ++j)
