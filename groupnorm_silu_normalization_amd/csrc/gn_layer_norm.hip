@@ -8,12 +8,13 @@
 //              dgamma[c] = sum over rows of dy*h, dbeta[c] = sum over rows of dy
 //
 // Both passes are bound by HBM: a row is read once, held in registers and
-// written once.  A row belongs to TPR lanes (a power of two within a wave, or
-// a whole workgroup), each holding NV pieces of W channels, so the two sums of
-// a row are a lane-group butterfly (plus, for a workgroup, one exchange of the
-// waves' sums through LDS).  The mean is taken first and the variance from the
-// differences: with the row in registers the second sum costs no memory
-// traffic, and no channel far from the rest can cancel it.
+// written once, and the next row's loads are in flight meanwhile.  A row
+// belongs to TPR lanes (a power of two, of one wave up to 64, of several
+// beyond), each holding NV pieces of W channels, so a row's sums are a
+// lane-group butterfly and, for several waves, one exchange of the waves' sums
+// through LDS.  The mean is taken first and the variance from the differences:
+// with the row in registers the second sum costs no memory traffic, and no
+// channel far from the rest can cancel it.
 //
 // The weight's gradients run down the columns.  A lane keeps the same channels
 // for every row it works on, so their sums stay in its registers over all of a
@@ -46,13 +47,13 @@ struct LnArgs {
     float *part;            // backward: [2][blocks][C] partial dgamma, dbeta, or null
     int64_t M, x_stride, dy_stride, y_stride;
     int C, P;
-    float eps;
+    float eps, inv_c;       // inv_c: 1 / C
     Affine af;
 };
 
-// The sum over a row's lanes.  A workgroup's row (TPR > 64) exchanges the
-// waves' sums through `red`; the caller passes a different part of it to
-// consecutive sums, so one barrier is enough.
+// The sums over a row's lanes.  A row of several waves exchanges their sums
+// through `red` (its workgroup has kSlots rows' of them); the caller passes a
+// different part of it to consecutive sums, so one barrier is enough.
 template <int TPR, int K>
 __device__ __forceinline__ void row_sum(float (&v)[K], float *red) {
     constexpr int N = TPR < 64 ? TPR : 64;
@@ -60,23 +61,24 @@ __device__ __forceinline__ void row_sum(float (&v)[K], float *red) {
     for (int k = 0; k < K; ++k) v[k] = lane_sum<N>(v[k]);
     if constexpr (TPR > 64) {
         constexpr int kWaves = TPR / 64;
-        const int wave = threadIdx.x >> 6;
+        float *mine = red + (threadIdx.x / TPR) * (K * kWaves);
+        const int wave = (threadIdx.x % TPR) >> 6;
         if ((threadIdx.x & 63) == 0) {
 #pragma unroll
-            for (int k = 0; k < K; ++k) red[k * kWaves + wave] = v[k];
+            for (int k = 0; k < K; ++k) mine[k * kWaves + wave] = v[k];
         }
         __syncthreads();
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            float s = red[k * kWaves];
+            float s = mine[k * kWaves];
 #pragma unroll
-            for (int w = 1; w < kWaves; ++w) s += red[k * kWaves + w];
+            for (int w = 1; w < kWaves; ++w) s += mine[k * kWaves + w];
             v[k] = s;
         }
     }
 }
 
-// Where the calling lane's piece j starts in its row and its first own
+// Where the calling lane's piece p starts in its row and its first own
 // channel; W for a lane beyond the row (it reads piece 0 and counts nothing).
 template <int W, bool TAIL>
 __device__ __forceinline__ void piece_at(const LnArgs &a, int p, int *c, int *lo) {
@@ -91,51 +93,101 @@ __device__ __forceinline__ void piece_at(const LnArgs &a, int p, int *c, int *lo
     }
 }
 
+// The value of a piece's channel i where it is the lane's own, else 0.  (A lane
+// beyond the row drops its whole sum.)
+template <bool TAIL> __device__ __forceinline__ float own(int i, int lo, float v) {
+    return !TAIL || i >= lo ? v : 0.0f;
+}
+
+// The rows of a row slot: base + slot, then one grid's worth of rows further,
+// each row's loads issued before the row ahead of it is worked on.  Slots
+// behind the last row read that row and do not store (the loop's end is the
+// same for the whole workgroup, which has barriers in it).
+template <class Row, int SLOTS> struct RowLoop {
+    int64_t M;
+    int slot;
+    Row a, b;
+    __device__ __forceinline__ int64_t row(int64_t base) const {
+        return base + slot < M ? base + slot : M - 1;
+    }
+    template <class Fetch> __device__ __forceinline__ void begin(Fetch &&fetch) {
+        fetch(a, row(int64_t{blockIdx.x} * SLOTS));
+    }
+    template <class Fetch, class Work>
+    __device__ __forceinline__ void run(Fetch &&fetch, Work &&work) {
+        const int64_t step = int64_t{gridDim.x} * SLOTS;
+        for (int64_t base = int64_t{blockIdx.x} * SLOTS;;) {
+            int64_t next = base + step;
+            if (next < M) fetch(b, row(next));
+            work(a, row(base), base + slot < M);
+            if (next >= M) break;
+            base = next;
+            next += step;
+            if (next < M) fetch(a, row(next));
+            work(b, row(base), base + slot < M);
+            if (next >= M) break;
+            base = next;
+        }
+    }
+};
+
 // ---------------------------------------------------------------------------
 // Forward.  Row slots per workgroup: THREADS / TPR.
 // ---------------------------------------------------------------------------
+template <class D, int W, int NV> struct ForwardRow {
+    Piece<D, W> v[NV];
+};
+
 template <class D, int W, bool TAIL, int TPR, int NV, int THREADS, bool SAVE>
 __global__ __launch_bounds__(THREADS) void gn_layer_norm(LnArgs a) {
     using T = typename D::storage;
     constexpr int kSlots = THREADS / TPR;
-    constexpr int kRed = TPR > 64 ? TPR / 64 : 1;
+    constexpr int kRed = TPR > 64 ? THREADS / 64 : 1;
     constexpr int kGroup = TPR < kBlock8 / W ? TPR : kBlock8 / W;
     __shared__ float red[2 * kRed];
-    const int t = threadIdx.x % TPR, slot = threadIdx.x / TPR;
+    const int t = threadIdx.x % TPR;
     const T *x = static_cast<const T *>(a.x);
     T *y = static_cast<T *>(a.y);
     int c[NV], lo[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) piece_at<W, TAIL>(a, t + j * TPR, &c[j], &lo[j]);
+    using Row = ForwardRow<D, W, NV>;
+    auto fetch = [&](Row &r, int64_t m) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) r.v[j].template load<false>(x + m * a.x_stride + c[j]);
+    };
+    RowLoop<Row, kSlots> loop{a.M, static_cast<int>(threadIdx.x / TPR)};
+    loop.begin(fetch);
     float ga[NV][W], be[NV][W];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-        piece_at<W, TAIL>(a, t + j * TPR, &c[j], &lo[j]);
         load_affine<W>(a.af.gamma, a.af.type, c[j], 1.0f, ga[j]);
         load_affine<W>(a.af.beta, a.af.type, c[j], 0.0f, be[j]);
     }
     const float fc = static_cast<float>(a.C);
     const int64_t nsb = (a.C + kBlock8 - 1) / kBlock8;
-    for (int64_t base = int64_t{blockIdx.x} * kSlots; base < a.M;
-         base += int64_t{gridDim.x} * kSlots) {
-        const bool live = base + slot < a.M;
-        const int64_t m = live ? base + slot : a.M - 1;
-        Piece<D, W> v[NV];
-#pragma unroll
-        for (int j = 0; j < NV; ++j) v[j].template load<false>(x + m * a.x_stride + c[j]);
+    loop.run(fetch, [&](const Row &r, int64_t m, bool live) {
         float s[1] = {0.0f};
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
+        for (int j = 0; j < NV; ++j) {
+            float p = 0.0f;
 #pragma unroll
-            for (int i = 0; i < W; ++i) s[0] += i >= lo[j] ? v[j].get(i) : 0.0f;
+            for (int i = 0; i < W; ++i) p += own<TAIL>(i, lo[j], r.v[j].get(i));
+            s[0] += lo[j] < W ? p : 0.0f;
+        }
         row_sum<TPR>(s, red);
         const float mean = s[0] / fc;
         float q[1] = {0.0f};
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
+        for (int j = 0; j < NV; ++j) {
+            float p = 0.0f;
 #pragma unroll
             for (int i = 0; i < W; ++i) {
-                const float d = i >= lo[j] ? v[j].get(i) - mean : 0.0f;
-                q[0] = fmaf(d, d, q[0]);
+                const float d = own<TAIL>(i, lo[j], r.v[j].get(i) - mean);
+                p = fmaf(d, d, p);
             }
+            q[0] += lo[j] < W ? p : 0.0f;
+        }
         row_sum<TPR>(q, red + kRed);
         const float rstd = 1.0f / sqrtf(q[0] / fc + a.eps);
         if (live && t == 0) {
@@ -147,127 +199,165 @@ __global__ __launch_bounds__(THREADS) void gn_layer_norm(LnArgs a) {
             float f[W], o[W];
 #pragma unroll
             for (int i = 0; i < W; ++i) {
-                f[i] = v[j].get(i);
+                f[i] = r.v[j].get(i);
                 o[i] = fmaf((f[i] - mean) * rstd, ga[j][i], be[j][i]);
             }
+            uint32_t E = 0;
+            if constexpr (SAVE)
+                E = block8_exponent<D, W, kGroup>(r.v[j], Magnitudes<D, W>(lo[j]));
+            if (!live || lo[j] >= W) continue;
             // A last piece's foreign channels get the value that their owner
             // writes, computed alike.
-            if (live && lo[j] < W) Piece<D, W>::template store<false>(y + m * a.y_stride + c[j], o);
-            if constexpr (SAVE) {
-                const uint32_t E = block8_exponent<D, W, kGroup>(v[j], Magnitudes<D, W>(lo[j]));
-                const Codes<W> qd = block8_encode<W>(f, E);
-                if (live && lo[j] < W)
-                    store_block8<W, TAIL, false>(qd, E, a.codes_out, a.scales_out, m * a.C, m * nsb,
-                                          c[j], lo[j]);
-            }
+            Piece<D, W>::template store<SAVE>(y + m * a.y_stride + c[j], o);
+            if constexpr (SAVE)
+                store_block8<W, TAIL, true>(block8_encode<W>(f, E), E, a.codes_out, a.scales_out,
+                                            m * a.C, m * nsb, c[j], lo[j]);
         }
-    }
+    });
 }
 
 // ---------------------------------------------------------------------------
 // Backward.  SAVED: x comes from its 8-bit checkpoint.
 // ---------------------------------------------------------------------------
+template <class D, int W, bool TAIL, int NV, bool SAVED> struct BackwardRow {
+    Piece<D, W> vx[SAVED ? 1 : NV], vy[NV];
+    Piece8<W, TAIL> v8[SAVED ? NV : 1];
+    float mean, rstd;
+    __device__ __forceinline__ void centred(int j, int c, float (&o)[W]) const {  // x - mean
+        if constexpr (SAVED) {
+            v8[j].widen_less(c, mean, o);
+        } else {
+#pragma unroll
+            for (int i = 0; i < W; ++i) o[i] = vx[j].get(i) - mean;
+        }
+    }
+    // Hides from the compiler that the row's values are those it has used, so
+    // that it does not keep what it made of them.
+    __device__ __forceinline__ void opaque() {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            if constexpr (SAVED)
+                v8[j].opaque();
+            else
+                vx[j].opaque();
+            vy[j].opaque();
+        }
+        asm volatile("" : "+v"(mean));
+    }
+};
+
 template <class D, int W, bool TAIL, int TPR, int NV, int THREADS, bool SAVED>
 __global__ __launch_bounds__(THREADS) void gn_layer_norm_backward(LnArgs a) {
     using T = typename D::storage;
     constexpr int kSlots = THREADS / TPR;
-    constexpr int kRed = TPR > 64 ? 2 * (TPR / 64) : 1;
+    constexpr int kRed = TPR > 64 ? 2 * (THREADS / 64) : 1;
     __shared__ float red[2 * kRed];
     const int t = threadIdx.x % TPR, slot = threadIdx.x / TPR;
     const T *x = static_cast<const T *>(a.x);
     const T *dy = static_cast<const T *>(a.dy);
     T *dx = static_cast<T *>(a.y);
     int c[NV], lo[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) piece_at<W, TAIL>(a, t + j * TPR, &c[j], &lo[j]);
+    const int64_t nsb = (a.C + kBlock8 - 1) / kBlock8;
+    using Row = BackwardRow<D, W, TAIL, NV, SAVED>;
+    auto fetch = [&](Row &r, int64_t m) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            if constexpr (SAVED)
+                r.v8[j].load(a.codes, a.scales, m * a.C, m * nsb, c[j]);
+            else
+                r.vx[j].template load<false>(x + m * a.x_stride + c[j]);
+            r.vy[j].template load<false>(dy + m * a.dy_stride + c[j]);
+        }
+        r.mean = a.mean[m];
+        r.rstd = a.rstd[m];
+    };
+    RowLoop<Row, kSlots> loop{a.M, slot};
+    loop.begin(fetch);
     float ga[NV][W], dg[NV][W], db[NV][W];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-        piece_at<W, TAIL>(a, t + j * TPR, &c[j], &lo[j]);
         load_affine<W>(a.af.gamma, a.af.type, c[j], 1.0f, ga[j]);
 #pragma unroll
         for (int i = 0; i < W; ++i) dg[j][i] = db[j][i] = 0.0f;
     }
-    const float fc = static_cast<float>(a.C);
-    const int64_t nsb = (a.C + kBlock8 - 1) / kBlock8;
     int par = 0;
-    for (int64_t base = int64_t{blockIdx.x} * kSlots; base < a.M;
-         base += int64_t{gridDim.x} * kSlots) {
-        const bool live = base + slot < a.M;
-        const int64_t m = live ? base + slot : a.M - 1;
-        Piece<D, W> vx[NV], vy[NV];
-        Piece8<W, TAIL> v8[NV];
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            if constexpr (SAVED)
-                v8[j].load(a.codes, a.scales, m * a.C, m * nsb, c[j]);
-            else
-                vx[j].template load<false>(x + m * a.x_stride + c[j]);
-            vy[j].template load<false>(dy + m * a.dy_stride + c[j]);
-        }
-        const float mean = a.mean[m], rstd = a.rstd[m];
-        float h[NV][W];
+    loop.run(fetch, [&](Row &r, int64_t m, bool live) {
+        // sums of g and of g*(x-mean); h = (x-mean)*rstd
         float s[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            if constexpr (SAVED) v8[j].widen(c[j], h[j]);
+            float x[W];
+            r.centred(j, c[j], x);
+            float p0 = 0.0f, p1 = 0.0f;
 #pragma unroll
             for (int i = 0; i < W; ++i) {
-                const float xv = SAVED ? h[j][i] : vx[j].get(i);
-                h[j][i] = (xv - mean) * rstd;
-                const float g = i >= lo[j] ? vy[j].get(i) * ga[j][i] : 0.0f;
-                s[0] += g;
-                // a select, not a product with a zero g: h may be NaN there
-                s[1] += i >= lo[j] ? g * h[j][i] : 0.0f;
+                const float g = r.vy[j].get(i) * ga[j][i];
+                p0 += own<TAIL>(i, lo[j], g);
+                if constexpr (TAIL)
+                    p1 += own<TAIL>(i, lo[j], g * x[i]);
+                else
+                    p1 = fmaf(g, x[i], p1);
             }
+            s[0] += lo[j] < W ? p0 : 0.0f;
+            s[1] += lo[j] < W ? p1 : 0.0f;
         }
         row_sum<TPR>(s, red + par * kRed);
         par ^= 1;
-        const float s0 = s[0] / fc, s1 = s[1] / fc;
+        if (!live) return;  // no barrier from here on
+        // The widened values are made again rather than kept across the sums:
+        // a dozen registers fewer, and with them twice the waves.
+        r.opaque();
+        const float s0 = s[0] * a.inv_c, s1 = r.rstd * r.rstd * (s[1] * a.inv_c);
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            float o[W];
+            float x[W], o[W];
+            r.centred(j, c[j], x);
 #pragma unroll
             for (int i = 0; i < W; ++i) {
-                const float d = vy[j].get(i);
-                o[i] = rstd * fmaf(-h[j][i], s1, fmaf(d, ga[j][i], -s0));
-                dg[j][i] = live ? fmaf(d, h[j][i], dg[j][i]) : dg[j][i];
-                db[j][i] = live ? db[j][i] + d : db[j][i];
+                const float d = r.vy[j].get(i);
+                o[i] = r.rstd * fmaf(-x[i], s1, fmaf(d, ga[j][i], -s0));
+                dg[j][i] = fmaf(d * r.rstd, x[i], dg[j][i]);
+                db[j][i] += d;
             }
-            if (live && lo[j] < W) Piece<D, W>::template store<false>(dx + m * a.y_stride + c[j], o);
+            if (lo[j] < W) Piece<D, W>::template store<true>(dx + m * a.y_stride + c[j], o);
         }
-    }
+    });
     if (a.part == nullptr) return;
     // The row slots of the workgroup: within a wave by butterflies over the
-    // lanes that hold the same channels, then wave by wave through LDS.
+    // lanes that hold the same channels, then slot by slot (wave by wave)
+    // through LDS.
     float *pg = a.part + int64_t{blockIdx.x} * a.C;
     float *pb = pg + int64_t{gridDim.x} * a.C;
     if constexpr (TPR >= 64) {
-        constexpr int kWaveSlots = kSlots;  // waves that hold the same channels
-        __shared__ float comb[kWaveSlots > 1 ? 2 * NV * W * 64 : 1];
+        constexpr int kPer = NV * W;
+        __shared__ float comb[kSlots > 1 ? 2 * kPer * TPR : 1];
 #pragma unroll 1
-        for (int w = 0; w < kWaveSlots; ++w) {
+        for (int w = 0; w < kSlots; ++w) {
             if (slot == w) {
 #pragma unroll
                 for (int j = 0; j < NV; ++j)
 #pragma unroll
                     for (int i = 0; i < W; ++i) {
-                        const int e = (j * W + i) * 64 + (threadIdx.x & 63);
-                        if constexpr (kWaveSlots > 1) {
+                        const int e = (j * W + i) * TPR + t;
+                        if constexpr (kSlots > 1) {
                             if (w > 0) {
                                 dg[j][i] += comb[e];
-                                db[j][i] += comb[NV * W * 64 + e];
+                                db[j][i] += comb[kPer * TPR + e];
                             }
-                            if (w + 1 < kWaveSlots) {
+                            if (w + 1 < kSlots) {
                                 comb[e] = dg[j][i];
-                                comb[NV * W * 64 + e] = db[j][i];
+                                comb[kPer * TPR + e] = db[j][i];
                             }
                         }
-                        if (w + 1 == kWaveSlots && i >= lo[j]) {
+                        if (w + 1 == kSlots && i >= lo[j]) {
                             pg[c[j] + i] = dg[j][i];
                             pb[c[j] + i] = db[j][i];
                         }
                     }
             }
-            if constexpr (kWaveSlots > 1) __syncthreads();
+            if constexpr (kSlots > 1) __syncthreads();
         }
     } else {
         static_assert(NV == 1, "rows of fewer lanes than a wave have one piece per lane");
@@ -305,107 +395,110 @@ __global__ __launch_bounds__(THREADS) void gn_layer_norm_backward(LnArgs a) {
     }
 }
 
-// dgamma and dbeta from the K partial rows of C sums: 64 channels and 16 row
-// parts per workgroup, each part's rows in order, then the parts in order, in
-// fp64.  K = 0 writes zeros.  blockIdx.y: 0 dgamma, 1 dbeta.
-constexpr int kColParts = 16;
-__global__ __launch_bounds__(64 * kColParts) void gn_column_sums(const float *part, int64_t K, int C,
-                                                                 void *dgamma, void *dbeta,
-                                                                 int type) {
-    __shared__ double red[kColParts][64];
+// dgamma and dbeta from the K partial rows of C sums: 32 channels and 32 row
+// parts per workgroup, each part's rows in order (eight rows' loads in
+// flight), then the parts by a fixed tree, in fp64.  K = 0 writes zeros.
+// blockIdx.y: 0 dgamma, 1 dbeta.
+constexpr int kColLanes = 32, kColParts = 32;
+__global__ __launch_bounds__(kColLanes *kColParts) void gn_column_sums(const float *part,
+                                                                        int64_t K, int C,
+                                                                        void *dgamma, void *dbeta,
+                                                                        int type) {
+    __shared__ double red[kColParts][kColLanes];
     void *out = blockIdx.y == 0 ? dgamma : dbeta;
     if (out == nullptr) return;
-    const int lane = threadIdx.x & 63, r = threadIdx.x >> 6;
-    const int c = static_cast<int>(blockIdx.x) * 64 + lane;
-    const float *p = part + static_cast<int64_t>(blockIdx.y) * K * C;
+    const int lane = threadIdx.x % kColLanes, r = threadIdx.x / kColLanes;
+    const int c = static_cast<int>(blockIdx.x) * kColLanes + lane;
+    const float *p = part + static_cast<int64_t>(blockIdx.y) * K * C + c;
     double s = 0.0;
     if (c < C) {
-#pragma unroll 8
-        for (int64_t k = r; k < K; k += kColParts) s += static_cast<double>(p[k * C + c]);
+        constexpr int kBatch = 8;
+        for (int64_t k = r; k < K; k += kBatch * kColParts) {
+            float v[kBatch];
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                const int64_t ku = k + u * kColParts;
+                v[u] = p[(ku < K ? ku : K - 1) * C];
+            }
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u)
+                s += k + u * kColParts < K ? static_cast<double>(v[u]) : 0.0;
+        }
     }
+    s += __shfl_xor(s, 32, 64);  // the wave's two parts
     red[r][lane] = s;
     __syncthreads();
-    if (r == 0 && c < C) {
-#pragma unroll
-        for (int i = 1; i < kColParts; ++i) s += red[i][lane];
-        store_affine(out, type, c, static_cast<float>(s));
+    for (int h = kColParts / 2; h > 1; h >>= 1) {  // even parts r < h + those at r + h
+        if (r < h) red[r][lane] = s += red[r + h][lane];
+        __syncthreads();
     }
+    if (r == 0 && c < C) store_affine(out, type, c, static_cast<float>(s));
 }
 
 // ---- host -----------------------------------------------------------------------
-constexpr int64_t kForwardBlocks = 2048;   // workgroups of 256 lanes: 8 per CU
-constexpr int64_t kBackwardBlocks = 512;   // 2 per CU: each writes a partial row
+// Workgroups: eight waves' worth of lanes per SIMD of 256 CUs forward, four
+// backward, where each workgroup writes a partial row.
+constexpr int64_t kForwardLanes = int64_t{2048} * 256;
+constexpr int64_t kBackwardBlocks = 256;  // one per CU
 
-// Lanes and pieces of a row: the fewest lanes of a wave that hold it with one
-// piece each, then up to four pieces per lane, then a workgroup per row.
+// Lanes of a row: the fewest (a power of two) that hold it with `nv` pieces
+// each.
 struct LnShape {
-    int w, tpr, nv, threads;
+    int w, tpr, nv;
     bool tail;
     int P;
-    int slots() const { return threads / tpr; }
 };
 
-LnShape ln_shape(int64_t C, int dtype) {
+LnShape ln_shape(int64_t C, int dtype, bool forward) {
     LnShape s;
     const int w = static_cast<int>(16 / elem_bytes(dtype));
     s.w = C < w ? 1 : w;
     s.tail = C % s.w != 0;
     s.P = static_cast<int>(ceil_div(C, s.w));
-    s.threads = 256;
-    if (s.P <= 64) {
-        s.nv = 1;
-        s.tpr = 1;
-        while (s.tpr < s.P) s.tpr *= 2;
-        if (s.w == 1) s.tpr = 8;
-    } else if (s.P <= 256) {
-        s.tpr = 64;
-        s.nv = s.P <= 128 ? 2 : 4;
-    } else if (s.P <= 1024) {
-        s.tpr = 256;
-        s.nv = s.P <= 512 ? 2 : 4;
-    } else {
-        s.tpr = s.threads = 512;
-        s.nv = s.P <= 2048 ? 4 : 8;
-    }
+    if (forward)
+        s.nv = s.P <= 64 ? 1 : (s.P <= 2048 ? 2 : 4);
+    else
+        s.nv = s.P <= 256 ? 1 : (s.P <= 1024 ? 2 : 4);
+    s.tpr = s.w == 1 ? 8 : 1;
+    while (s.tpr * s.nv < s.P) s.tpr *= 2;
     return s;
 }
 
 template <int V> using IC = std::integral_constant<int, V>;
 
-// Calls f(IC<W>, IC<TAIL>, IC<TPR>, IC<NV>, IC<THREADS>).
-template <class D, class F>
+// Calls f(IC<W>, IC<TAIL>, IC<TPR>, IC<NV>).
+template <class D, bool FORWARD, class F>
 void with_ln_shape(const LnShape &s, F &&f) {
     constexpr int W = static_cast<int>(16 / sizeof(typename D::storage));
-    if (s.w == 1) {
-        f(IC<1>{}, IC<0>{}, IC<8>{}, IC<1>{}, IC<256>{});
-        return;
-    }
+    if (s.w == 1) return f(IC<1>{}, IC<0>{}, IC<8>{}, IC<1>{});
     auto by_tail = [&](auto tail) {
-        if (s.tpr == 512) {
-            if (s.nv == 4)
-                f(IC<W>{}, tail, IC<512>{}, IC<4>{}, IC<512>{});
-            else if constexpr (W == 4)
-                f(IC<W>{}, tail, IC<512>{}, IC<8>{}, IC<512>{});
-            return;
+        if (s.nv == 1) {
+            switch (s.tpr) {
+                case 1: return f(IC<W>{}, IC<0>{}, IC<1>{}, IC<1>{});  // P = 1: C = W
+                case 2: return f(IC<W>{}, tail, IC<2>{}, IC<1>{});
+                case 4: return f(IC<W>{}, tail, IC<4>{}, IC<1>{});
+                case 8: return f(IC<W>{}, tail, IC<8>{}, IC<1>{});
+                case 16: return f(IC<W>{}, tail, IC<16>{}, IC<1>{});
+                case 32: return f(IC<W>{}, tail, IC<32>{}, IC<1>{});
+                case 64: return f(IC<W>{}, tail, IC<64>{}, IC<1>{});
+            }
+            if constexpr (!FORWARD) {
+                if (s.tpr == 128) return f(IC<W>{}, tail, IC<128>{}, IC<1>{});
+                return f(IC<W>{}, tail, IC<256>{}, IC<1>{});
+            }
         }
-        if (s.tpr == 256) {
-            if (s.nv == 2)
-                f(IC<W>{}, tail, IC<256>{}, IC<2>{}, IC<256>{});
-            else
-                f(IC<W>{}, tail, IC<256>{}, IC<4>{}, IC<256>{});
-            return;
+        if (s.nv == 2) {
+            if constexpr (FORWARD) {
+                if (s.tpr == 64) return f(IC<W>{}, tail, IC<64>{}, IC<2>{});
+                if (s.tpr == 128) return f(IC<W>{}, tail, IC<128>{}, IC<2>{});
+                if (s.tpr == 1024) return f(IC<W>{}, tail, IC<1024>{}, IC<2>{});
+            }
+            if (s.tpr == 256) return f(IC<W>{}, tail, IC<256>{}, IC<2>{});
+            return f(IC<W>{}, tail, IC<512>{}, IC<2>{});
         }
-        if (s.nv == 4) return f(IC<W>{}, tail, IC<64>{}, IC<4>{}, IC<256>{});
-        if (s.nv == 2) return f(IC<W>{}, tail, IC<64>{}, IC<2>{}, IC<256>{});
-        switch (s.tpr) {
-            case 1: return f(IC<W>{}, IC<0>{}, IC<1>{}, IC<1>{}, IC<256>{});  // P = 1: C = W
-            case 2: return f(IC<W>{}, tail, IC<2>{}, IC<1>{}, IC<256>{});
-            case 4: return f(IC<W>{}, tail, IC<4>{}, IC<1>{}, IC<256>{});
-            case 8: return f(IC<W>{}, tail, IC<8>{}, IC<1>{}, IC<256>{});
-            case 16: return f(IC<W>{}, tail, IC<16>{}, IC<1>{}, IC<256>{});
-            case 32: return f(IC<W>{}, tail, IC<32>{}, IC<1>{}, IC<256>{});
-            default: return f(IC<W>{}, tail, IC<64>{}, IC<1>{}, IC<256>{});
-        }
+        if constexpr (!FORWARD)
+            if (s.tpr == 512) return f(IC<W>{}, tail, IC<512>{}, IC<4>{});
+        if constexpr (W == 4) f(IC<W>{}, tail, IC<1024>{}, IC<4>{});
     };
     if (s.tail)
         by_tail(IC<1>{});
@@ -413,12 +506,16 @@ void with_ln_shape(const LnShape &s, F &&f) {
         by_tail(IC<0>{});
 }
 
+constexpr int forward_threads(int tpr) { return tpr < 256 ? 256 : tpr; }
+constexpr int backward_threads(int tpr, int nv) { return nv == 1 || tpr > 512 ? 1024 : 512; }
+
 template <class D>
 void launch_forward(const LnShape &s, const LnArgs &a, hipStream_t st) {
-    const int64_t blocks = std::min(ceil_div(a.M, s.slots()), kForwardBlocks * 256 / s.threads);
-    with_ln_shape<D>(s, [&](auto w, auto tail, auto tpr, auto nv, auto nt) {
+    const int nt = forward_threads(s.tpr);
+    const int64_t blocks = std::min(ceil_div(a.M, nt / s.tpr), kForwardLanes / nt);
+    with_ln_shape<D, true>(s, [&](auto w, auto tail, auto tpr, auto nv) {
         constexpr int W = decltype(w)::value, TPR = decltype(tpr)::value;
-        constexpr int NV = decltype(nv)::value, NT = decltype(nt)::value;
+        constexpr int NV = decltype(nv)::value, NT = forward_threads(TPR);
         constexpr bool TAIL = decltype(tail)::value != 0;
         const dim3 grid(static_cast<unsigned>(blocks)), block(NT);
         if (a.codes_out != nullptr)
@@ -429,15 +526,15 @@ void launch_forward(const LnShape &s, const LnArgs &a, hipStream_t st) {
 }
 
 int64_t backward_blocks(const LnShape &s, int64_t M) {
-    return std::min(ceil_div(M, s.slots()), kBackwardBlocks * 256 / s.threads);
+    return std::min(ceil_div(M, backward_threads(s.tpr, s.nv) / s.tpr), kBackwardBlocks);
 }
 
 template <class D>
 void launch_backward(const LnShape &s, const LnArgs &a, hipStream_t st) {
     const int64_t blocks = backward_blocks(s, a.M);
-    with_ln_shape<D>(s, [&](auto w, auto tail, auto tpr, auto nv, auto nt) {
+    with_ln_shape<D, false>(s, [&](auto w, auto tail, auto tpr, auto nv) {
         constexpr int W = decltype(w)::value, TPR = decltype(tpr)::value;
-        constexpr int NV = decltype(nv)::value, NT = decltype(nt)::value;
+        constexpr int NV = decltype(nv)::value, NT = backward_threads(TPR, NV);
         constexpr bool TAIL = decltype(tail)::value != 0;
         const dim3 grid(static_cast<unsigned>(blocks)), block(NT);
         if (a.codes != nullptr)
@@ -483,7 +580,7 @@ gn_status check_ln(int64_t M, int64_t C, int dtype, const int64_t *in_strides, i
 
 size_t backward_workspace(int64_t M, int64_t C, int dtype) {
     if (M == 0) return 0;
-    return sizeof(float) * 2 * static_cast<size_t>(backward_blocks(ln_shape(C, dtype), M)) *
+    return sizeof(float) * 2 * static_cast<size_t>(backward_blocks(ln_shape(C, dtype, false), M)) *
            static_cast<size_t>(C);
 }
 
@@ -513,7 +610,7 @@ gn_status gn_layer_norm_rows(const void *x, int64_t x_stride, const void *gamma,
     st = begin_call(stream,
                     {x, gamma, beta, y, mean_out, rstd_out, codes_out, scales_out}, &c);
     if (st != GN_OK) return st;
-    const LnShape s = ln_shape(C, dtype);
+    const LnShape s = ln_shape(C, dtype, true);
     LnArgs a{};
     a.x = x;
     a.y = y;
@@ -573,7 +670,7 @@ gn_status gn_layer_norm_rows_backward(const void *dy, int64_t dy_stride, const v
                      need > 0 ? workspace : nullptr},
                     &c);
     if (st != GN_OK) return st;
-    const LnShape s = ln_shape(C, dtype);
+    const LnShape s = ln_shape(C, dtype, false);
     LnArgs a{};
     a.x = x;
     a.codes = static_cast<const int8_t *>(codes);
@@ -589,11 +686,12 @@ gn_status gn_layer_norm_rows_backward(const void *dy, int64_t dy_stride, const v
     a.y_stride = dx_stride;
     a.C = static_cast<int>(C);
     a.P = s.P;
+    a.inv_c = 1.0f / static_cast<float>(C);
     a.af = Affine{gamma, nullptr, affine_type(dtype)};
     if (M > 0) by_type(dtype, [&](auto d) { launch_backward<decltype(d)>(s, a, c.stream); });
     if (grads)
-        gn_column_sums<<<dim3(static_cast<unsigned>(ceil_div(C, 64)), 2), 64 * kColParts, 0,
-                         c.stream>>>(static_cast<const float *>(workspace),
+        gn_column_sums<<<dim3(static_cast<unsigned>(ceil_div(C, kColLanes)), 2),
+                         kColLanes * kColParts, 0, c.stream>>>(static_cast<const float *>(workspace),
                                      M > 0 ? backward_blocks(s, M) : 0, a.C, dgamma, dbeta,
                                      a.af.type);
     return finish_launch();

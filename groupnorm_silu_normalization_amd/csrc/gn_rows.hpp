@@ -38,6 +38,7 @@ template <class D> struct Piece16x8 {
     __device__ __forceinline__ float get(int j) const {
         return (j & 1) ? D::hi(w[j >> 1]) : D::lo(w[j >> 1]);
     }
+    __device__ __forceinline__ void opaque() { asm volatile("" : "+v"(w)); }
     template <bool NT>
     __device__ __forceinline__ void load(const uint16_t *p) {
         if constexpr (NT)
@@ -62,6 +63,7 @@ template <> struct Piece<Fp16, 8> : Piece16x8<Fp16> {};
 template <> struct Piece<F32, 4> {
     u32x4 w;
     __device__ __forceinline__ float get(int j) const { return __uint_as_float(w[j]); }
+    __device__ __forceinline__ void opaque() { asm volatile("" : "+v"(w)); }
     template <bool NT>
     __device__ __forceinline__ void load(const float *p) {
         if constexpr (NT)
@@ -84,6 +86,7 @@ template <> struct Piece<F32, 4> {
 template <class D> struct Piece<D, 1> {
     typename D::storage b;
     __device__ __forceinline__ float get(int) const { return D::to_f32(b); }
+    __device__ __forceinline__ void opaque() {}
     template <bool NT>
     __device__ __forceinline__ void load(const typename D::storage *p) { b = ld<NT>(p); }
     template <bool NT>
@@ -234,6 +237,7 @@ template <> struct Codes<8> {
         return static_cast<int8_t>(w[j >> 2] >> (8 * (j & 3)));
     }
     __device__ __forceinline__ void set4(int q, uint32_t v) { w[q] = v; }
+    __device__ __forceinline__ void opaque() { asm volatile("" : "+v"(w)); }
 };
 template <> struct Codes<4> {
     uint32_t w;
@@ -248,6 +252,7 @@ template <> struct Codes<4> {
     }
     __device__ __forceinline__ int get(int j) const { return static_cast<int8_t>(w >> (8 * j)); }
     __device__ __forceinline__ void set4(int, uint32_t v) { w = v; }
+    __device__ __forceinline__ void opaque() { asm volatile("" : "+v"(w)); }
 };
 template <> struct Codes<1> {
     uint32_t w;
@@ -256,6 +261,7 @@ template <> struct Codes<1> {
         *p = static_cast<int8_t>(w);
     }
     __device__ __forceinline__ int get(int) const { return static_cast<int8_t>(w); }
+    __device__ __forceinline__ void opaque() {}
 };
 
 // A piece of saved values: its codes and the scale bytes of its first and last
@@ -282,6 +288,13 @@ template <int W, bool TAIL> struct Piece8 {
 #pragma unroll
             for (int j = 0; j < W; ++j) o[j] = static_cast<float>(q.get(j)) * s0;
         }
+    }
+    __device__ __forceinline__ void opaque() { q.opaque(); }
+    __device__ __forceinline__ void widen_less(int c, float mu, float (&o)[W]) const {
+        float m[W];
+#pragma unroll
+        for (int j = 0; j < W; ++j) m[j] = mu;
+        widen_less(c, m, o);
     }
     // The values less mu, in one fma each.
     __device__ __forceinline__ void widen_less(int c, const float (&mu)[W], float (&o)[W]) const {
