@@ -39,6 +39,7 @@ gn_device_info).
 """
 import ctypes
 import enum
+import functools
 import math
 import os
 
@@ -399,11 +400,11 @@ def apply_rows(x, mean, rstd, weight=None, bias=None, apply_silu=True, out=None,
     checkpoint: also return x's 8-bit checkpoint, written in the same pass
     ((y, Checkpoint8) instead of y; any C up to MAX_CHANNELS), for
     ``group_norm_silu_rows_backward``."""
+    if checkpoint:
+        return _apply_rows_save(x, mean, rstd, weight, bias, apply_silu, out)
     torch = _torch()
     N, L, C = x.shape
     G = mean.shape[-1]
-    if checkpoint:
-        return _apply_rows_save(x, mean, rstd, weight, bias, apply_silu, out, N, L, C, G)
     if out is None:
         out = torch.empty_like(x)
     code = lib.gn_apply_rows_dtype(_ptr(x), _ptr(mean), _ptr(rstd), _ptr(weight), _ptr(bias),
@@ -479,6 +480,25 @@ def _dense_like(x):
     return torch.empty_like(x, memory_format=torch.contiguous_format)
 
 
+def _run(fn, t, *args):
+    """fn(*args, current stream of t's device), with that device current: the
+    null stream's handle does not say whose it is."""
+    torch = _torch()
+    dev = t.device.index
+    if dev == torch.cuda.current_device():
+        return fn(*args, _stream_handle(t))
+    with torch.cuda.device(dev):
+        return fn(*args, _stream_handle(t))
+
+
+@functools.lru_cache(maxsize=256)
+def _workspace_bytes(name, *args):
+    """Workspace size of a backward call's shape, or None if it is declined."""
+    need = _i64(0)
+    code = getattr(lib, name)(*args, ctypes.byref(need))
+    return None if _result(code, True) is None else need.value
+
+
 def _addr(t):
     """A tensor's address for a void pointer argument, None for none."""
     return None if t is None else t.data_ptr()
@@ -520,8 +540,8 @@ def checkpoint_rows(x):
     if step is None or x.shape[-1] == 0:
         return None
     ck = _empty_checkpoint(x.shape, x.device, x.dtype)
-    code = lib.gn_checkpoint_rows(_addr(x), step, _addr(ck.codes), _addr(ck.scales), _rows_of(x),
-                                  x.shape[-1], dtype_code(x.dtype), _stream_handle(x))
+    code = _run(lib.gn_checkpoint_rows, x, _addr(x), step, _addr(ck.codes), _addr(ck.scales),
+                _rows_of(x), x.shape[-1], dtype_code(x.dtype))
     return _result(code, ck) if x.numel() else ck
 
 
@@ -547,9 +567,8 @@ def restore_rows(checkpoint, dtype=None, out=None):
         return None
     if not out.numel():
         return out
-    code = lib.gn_restore_rows(_addr(codes), _addr(checkpoint.scales), _addr(out), step,
-                               _rows_of(codes), codes.shape[-1], dtype_code(out.dtype),
-                               _stream_handle(codes))
+    code = _run(lib.gn_restore_rows, codes, _addr(codes), _addr(checkpoint.scales), _addr(out),
+                step, _rows_of(codes), codes.shape[-1], dtype_code(out.dtype))
     return _result(code, out)
 
 
@@ -590,10 +609,10 @@ def layer_norm_rows(x, weight=None, bias=None, eps=1e-6, *, stats=False, checkpo
     r = (out, mean, rstd, ck) if checkpoint else (out, mean, rstd) if stats else out
     if not x.numel():
         return r
-    code = lib.gn_layer_norm_rows(
-        _addr(x), step, _addr(weight), _addr(bias), _addr(out), ostep, _rows_of(x), C, float(eps),
-        dtype_code(x.dtype) | affine, _addr(mean), _addr(rstd), _addr(ck.codes if ck else None),
-        _addr(ck.scales if ck else None), _stream_handle(x))
+    code = _run(
+        lib.gn_layer_norm_rows, x, _addr(x), step, _addr(weight), _addr(bias), _addr(out), ostep,
+        _rows_of(x), C, float(eps), dtype_code(x.dtype) | affine, _addr(mean), _addr(rstd),
+        _addr(ck.codes) if ck else None, _addr(ck.scales) if ck else None)
     return _result(code, r)
 
 
@@ -659,25 +678,43 @@ def layer_norm_rows_backward(dy, x, mean, rstd, weight=None, *, weight_grad=True
     dtype = dtype_code(dy.dtype) | _affine_flag(weight, None)
     ws, size = None, 0
     if weight_grad:
-        need = _i64(0)
-        _result(lib.gn_layer_norm_rows_backward_workspace(M, C, dtype, ctypes.byref(need)), None)
-        size = need.value
+        size = _workspace_bytes("gn_layer_norm_rows_backward_workspace", M, C, dtype)
+        if size is None:
+            return None
         ws = torch.empty(size, dtype=torch.uint8, device=dy.device)
-    code = lib.gn_layer_norm_rows_backward(
-        _addr(dy), step, xp, xstep, codes, scales, _addr(mean), _addr(rstd), _addr(weight), _addr(out),
-        ostep, _addr(dw), _addr(db), M, C, dtype, _addr(ws), size, _stream_handle(dy))
+    code = _run(
+        lib.gn_layer_norm_rows_backward, dy, _addr(dy), step, xp, xstep, codes, scales,
+        _addr(mean), _addr(rstd), _addr(weight), _addr(out), ostep, _addr(dw), _addr(db), M, C,
+        dtype, _addr(ws), size)
     return _result(code, (out, dw, db))
 
 
-def _apply_rows_save(x, mean, rstd, weight, bias, apply_silu, out, N, L, C, G):
-    torch = _torch()
+def _apply_rows_save(x, mean, rstd, weight, bias, apply_silu, out):
+    if not _gpu_rows(x):
+        return None
+    if x.dim() != 3:
+        raise ValueError("apply_rows expects a 3-D (N, L, C) tensor, got %d-D" % x.dim())
+    N, L, C = x.shape
+    G = mean.shape[-1]
+    if C > 0:
+        _check_groups(C, G)
+    ok = _stat(mean, N * G, "mean", x)
+    ok = _stat(rstd, N * G, "rstd", x) and ok
+    ok = _affine_ok(weight, C, x.device, "weight") and ok
+    ok = _affine_ok(bias, C, x.device, "bias") and ok
+    if not ok or C == 0 or C > MAX_CHANNELS or not x.is_contiguous():
+        return None
     if out is None:
         out = _dense_like(x)
+    else:
+        _check_out(out, x)
+        if not out.is_contiguous():
+            raise ValueError("out must be contiguous")
     ck = _empty_checkpoint(x.shape, x.device, x.dtype)
-    code = lib.gn_apply_rows_save(
-        _addr(x), _addr(mean), _addr(rstd), _addr(weight), _addr(bias), _addr(out), _addr(ck.codes),
-        _addr(ck.scales), N, L, C, G, 1 if apply_silu else 0,
-        _dtype_arg(x) | _affine_arg(weight, bias), _stream_handle(x))
+    code = _run(
+        lib.gn_apply_rows_save, x, _addr(x), _addr(mean), _addr(rstd), _addr(weight), _addr(bias),
+        _addr(out), _addr(ck.codes), _addr(ck.scales), N, L, C, G, 1 if apply_silu else 0,
+        _dtype_arg(x) | _affine_arg(weight, bias))
     return _result(code, (out, ck))
 
 
@@ -726,15 +763,14 @@ def group_norm_silu_rows_backward(dy, x, mean, rstd, weight=None, bias=None, app
             db.zero_()
         return out, dw, db
     dtype = dtype_code(dy.dtype) | affine
-    need = _i64(0)
-    code = lib.gn_silu_rows_backward_workspace(N, L, C, G, dtype, ctypes.byref(need))
-    if _result(code, True) is None:
+    size = _workspace_bytes("gn_silu_rows_backward_workspace", N, L, C, G, dtype)
+    if size is None:
         return None
-    ws = torch.empty(need.value, dtype=torch.uint8, device=dy.device)
-    code = lib.gn_silu_rows_backward(
-        _addr(dy), xp, codes, scales, _addr(mean), _addr(rstd), _addr(weight), _addr(bias), _addr(out),
-        _addr(dw), _addr(db), N, L, C, G, 1 if apply_silu else 0, dtype, _addr(ws), need.value,
-        _stream_handle(dy))
+    ws = torch.empty(size, dtype=torch.uint8, device=dy.device)
+    code = _run(
+        lib.gn_silu_rows_backward, dy, _addr(dy), xp, codes, scales, _addr(mean), _addr(rstd),
+        _addr(weight), _addr(bias), _addr(out), _addr(dw), _addr(db), N, L, C, G,
+        1 if apply_silu else 0, dtype, _addr(ws), size)
     return _result(code, (out, dw, db))
 
 

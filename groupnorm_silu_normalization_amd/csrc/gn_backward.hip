@@ -90,31 +90,31 @@ template <int W, bool TAIL> struct Place {
 
 // A workgroup's batches k, k + K, ...: the workgroups together move through
 // the sample as one front, and while a batch is worked on the next one's
-// loads are in flight.  `load` takes rows that exist (rows behind the last one
-// are read as the last one and not worked on).  BACK: from the sample's end.
+// loads are in flight.  load(v, d) and work(v, d, live) take the row that lies
+// d rows behind the lane's row slot; rows behind the sample's last one are
+// read as that one and not live.  BACK: from the sample's end.
 template <bool BACK, int U, class V> struct Stream {
     const Tiles &tl;
     int64_t r;
     V a[U], b[U];
     __device__ __forceinline__ Stream(const Tiles &t, int row_slot) : tl(t), r(row_slot) {}
-    __device__ __forceinline__ int64_t row(int64_t i, int u) const {
-        return ((BACK ? tl.batches - 1 - i : i) * U + u) * tl.R + r;
+    __device__ __forceinline__ int64_t first(int64_t i) const {
+        return (BACK ? tl.batches - 1 - i : i) * (U * tl.R);
     }
     template <class Load>
     __device__ __forceinline__ void fetch(V (&v)[U], int64_t i, Load &&load) {
+        const int64_t d = first(i);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int64_t l = row(i, u);
-            load(v[u], l < tl.L ? l : tl.L - 1);
+            const int64_t l = d + u * tl.R + r;
+            load(v[u], (l < tl.L ? l : tl.L - 1) - r);
         }
     }
     template <class Work>
     __device__ __forceinline__ void work(const V (&v)[U], int64_t i, Work &&w) {
+        const int64_t d = first(i);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t l = row(i, u);
-            w(v[u], l, l < tl.L);
-        }
+        for (int u = 0; u < U; ++u) w(v[u], d + u * tl.R, d + u * tl.R + r < tl.L);
     }
     // The first batch's loads; before the loads of the channel parameters, so
     // that their round trips overlap.
@@ -166,17 +166,30 @@ template <class D, int W, bool TAIL, bool SAVED> struct Pair {
     using T = typename D::storage;
     Piece<D, W> vx, vy;
     Piece8<W, TAIL> v8;
-    __device__ __forceinline__ void load(const RowArgs &a, int64_t row, int64_t nsb, int c) {
+    // The lane's piece of its row slot's first row; d rows further is a scalar
+    // away.
+    struct From {
+        const T *x, *dy;
+        Piece8At<W, TAIL> at8;
+        int64_t C, nsb;
+        __device__ __forceinline__ From(const RowArgs &a, int64_t row, int c)
+            : x(static_cast<const T *>(a.x) + row * a.tl.C + c),
+              dy(static_cast<const T *>(a.dy) + row * a.tl.C + c),
+              at8(a.codes, a.scales, row, a.tl.C, c), C(a.tl.C),
+              nsb((a.tl.C + kBlock8 - 1) / kBlock8) {}
+    };
+    __device__ __forceinline__ void load(const From &f, int64_t d) {
         if constexpr (SAVED)
-            v8.load(a.codes, a.scales, row * a.tl.C, row * nsb, c);
+            v8.load(f.at8, d * f.C, d * f.nsb);
         else
-            vx.template load<false>(static_cast<const T *>(a.x) + row * a.tl.C + c);
-        vy.template load<false>(static_cast<const T *>(a.dy) + row * a.tl.C + c);
+            vx.template load<false>(f.x + d * f.C);
+        vy.template load<false>(f.dy + d * f.C);
     }
     // x - mean: a saved value is widened and shifted in one fma
-    __device__ __forceinline__ void centred(int c, const float (&mu)[W], float (&o)[W]) const {
+    __device__ __forceinline__ void centred(int c, const float (&mu)[W], bool edge,
+                                            float (&o)[W]) const {
         if constexpr (SAVED) {
-            v8.widen_less(c, mu, o);
+            v8.widen_less(c, mu, edge, o);
         } else {
 #pragma unroll
             for (int i = 0; i < W; ++i) o[i] = vx.get(i) - mu[i];
@@ -210,10 +223,11 @@ __global__ __launch_bounds__(NT) void gn_grad_sums(RowArgs a) {
     __shared__ float red[W][NT];
     const Tiles &tl = a.tl;
     const Place<W, TAIL> at(tl);
-    const int64_t nsb = (tl.C + kBlock8 - 1) / kBlock8;
-    const int64_t row0 = at.n * tl.L;
+    const int64_t row0 = at.n * tl.L + at.r;
     using V = Pair<D, W, TAIL, SAVED>;
-    auto load = [&](V &v, int64_t l) { v.load(a, row0 + l, nsb, at.c); };
+    const typename V::From from(a, row0, at.c);
+    auto load = [&](V &v, int64_t d) { v.load(from, d); };
+    const bool edge = SAVED && wave_has_edge<W, TAIL>(at.lo);
     Stream<false, kUnroll, V> st(tl, at.r);
     st.begin(at.k, load);
     Channels<W> ch;
@@ -224,7 +238,7 @@ __global__ __launch_bounds__(NT) void gn_grad_sums(RowArgs a) {
     st.run(at.k, load, [&](const V &v, int64_t, bool live) {
         if (!live) return;
         float x[W];
-        v.centred(at.c, ch.mu, x);
+        v.centred(at.c, ch.mu, edge, x);
 #pragma unroll
         for (int i = 0; i < W; ++i) {
             float d = v.vy.get(i);
@@ -397,10 +411,11 @@ __global__ __launch_bounds__(kLanes) void gn_grad_input(RowArgs a) {
     using T = typename D::storage;
     const Tiles &tl = a.tl;
     const Place<W, TAIL> at(tl);
-    const int64_t nsb = (tl.C + kBlock8 - 1) / kBlock8;
-    const int64_t row0 = at.n * tl.L;
+    const int64_t row0 = at.n * tl.L + at.r;
     using V = Pair<D, W, TAIL, SAVED>;
-    auto load = [&](V &v, int64_t l) { v.load(a, row0 + l, nsb, at.c); };
+    const typename V::From from(a, row0, at.c);
+    auto load = [&](V &v, int64_t d) { v.load(from, d); };
+    const bool edge = SAVED && wave_has_edge<W, TAIL>(at.lo);
     Stream<true, SAVED ? kUnroll : kInputUnroll, V> st(tl, at.r);
     st.begin(at.k, load);
     Channels<W> ch;
@@ -412,17 +427,18 @@ __global__ __launch_bounds__(kLanes) void gn_grad_input(RowArgs a) {
         k0[i] = -ch.rs[i] * co[0];
         k1[i] = -ch.rs[i] * ch.rs[i] * co[1];
     }
-    st.run(at.k, load, [&](const V &v, int64_t l, bool live) {
+    T *dx = static_cast<T *>(a.y) + row0 * tl.C + at.c;
+    st.run(at.k, load, [&](const V &v, int64_t d, bool live) {
         if (!live || !at.active) return;
         float x[W], o[W];
-        v.centred(at.c, ch.mu, x);
+        v.centred(at.c, ch.mu, edge, x);
 #pragma unroll
         for (int i = 0; i < W; ++i) {
-            float d = v.vy.get(i);
-            if constexpr (SILU) d = silu_grad(fmaf(x[i], ch.sc[i], ch.be[i]), d);
-            o[i] = fmaf(d, ch.sc[i], fmaf(x[i], k1[i], k0[i]));
+            float g = v.vy.get(i);
+            if constexpr (SILU) g = silu_grad(fmaf(x[i], ch.sc[i], ch.be[i]), g);
+            o[i] = fmaf(g, ch.sc[i], fmaf(x[i], k1[i], k0[i]));
         }
-        T *p = static_cast<T *>(a.y) + (row0 + l) * tl.C + at.c;
+        T *p = dx + d * tl.C;
         // dx may be dy or x: a lane writes only channels that no other reads
         if (!TAIL || at.lo == 0)
             Piece<D, W>::template store<true>(p, o);
@@ -442,11 +458,10 @@ __global__ __launch_bounds__(kLanes) void gn_rows_save(RowArgs a) {
     const Tiles &tl = a.tl;
     const Place<W, TAIL> at(tl);
     const int64_t nsb = (tl.C + kBlock8 - 1) / kBlock8;
-    const int64_t row0 = at.n * tl.L;
+    const int64_t row0 = at.n * tl.L + at.r;
     using V = Piece<D, W>;
-    auto load = [&](V &v, int64_t l) {
-        v.template load<false>(static_cast<const T *>(a.x) + (row0 + l) * a.x_stride + at.c);
-    };
+    const T *x0 = static_cast<const T *>(a.x) + row0 * a.x_stride + at.c;
+    auto load = [&](V &v, int64_t d) { v.template load<false>(x0 + d * a.x_stride); };
     Stream<false, kUnroll, V> st(tl, at.r);
     st.begin(at.k, load);
     float sc[W], sh[W];
@@ -460,9 +475,11 @@ __global__ __launch_bounds__(kLanes) void gn_rows_save(RowArgs a) {
         }
     }
     const Magnitudes<D, W> mag(at.active ? at.lo : W);
+    int8_t *codes0 = a.codes_out + row0 * tl.C;
+    uint8_t *scales0 = a.scales_out + row0 * nsb;
+    T *y0 = static_cast<T *>(a.y) + row0 * a.y_stride + at.c;
     // every lane of the workgroup takes part in the blocks' maxima
-    st.run(at.k, load, [&](const V &v, int64_t l, bool live) {
-        const int64_t row = row0 + l;
+    st.run(at.k, load, [&](const V &v, int64_t d, bool live) {
         float x[W];
 #pragma unroll
         for (int i = 0; i < W; ++i) x[i] = v.get(i);
@@ -475,14 +492,14 @@ __global__ __launch_bounds__(kLanes) void gn_rows_save(RowArgs a) {
                 const float t = fmaf(x[i], sc[i], sh[i]);
                 o[i] = MODE == kApplySilu ? silu_f32(t) : t;
             }
-            T *p = static_cast<T *>(a.y) + row * a.y_stride + at.c;
+            T *p = y0 + d * a.y_stride;
             if (!TAIL || at.lo == 0)  // y may be x: only the lane's own channels
                 Piece<D, W>::template store<true>(p, o);
             else
                 store_from<D, W>(p, o, at.lo);
         }
-        store_block8<W, TAIL, true>(block8_encode<W>(x, E), E, a.codes_out, a.scales_out,
-                                    row * tl.C, row * nsb, at.c, at.lo);
+        store_block8<W, TAIL, true>(block8_encode<W>(x, E), E, codes0 + d * tl.C,
+                                    scales0 + d * nsb, at.c, at.lo);
     });
 }
 
@@ -493,19 +510,19 @@ __global__ __launch_bounds__(kLanes) void gn_rows_restore(RowArgs a) {
     const Tiles &tl = a.tl;
     const Place<W, TAIL> at(tl);
     const int64_t nsb = (tl.C + kBlock8 - 1) / kBlock8;
-    const int64_t row0 = at.n * tl.L;
+    const int64_t row0 = at.n * tl.L + at.r;
     using V = Piece8<W, TAIL>;
-    auto load = [&](V &v, int64_t l) {
-        v.load(a.codes, a.scales, (row0 + l) * tl.C, (row0 + l) * nsb, at.c);
-    };
+    const Piece8At<W, TAIL> from(a.codes, a.scales, row0, tl.C, at.c);
+    auto load = [&](V &v, int64_t d) { v.load(from, d * tl.C, d * nsb); };
+    const bool edge = wave_has_edge<W, TAIL>(at.lo);
+    T *y0 = static_cast<T *>(a.y) + row0 * a.y_stride + at.c;
     Stream<false, kUnroll, V> st(tl, at.r);
     st.begin(at.k, load);
-    st.run(at.k, load, [&](const V &v, int64_t l, bool live) {
+    st.run(at.k, load, [&](const V &v, int64_t d, bool live) {
         if (!live || !at.active) return;
         float o[W];
-        v.widen(at.c, o);
-        Piece<D, W>::template store<true>(
-            static_cast<T *>(a.y) + (row0 + l) * a.y_stride + at.c, o);
+        v.widen(at.c, edge, o);
+        Piece<D, W>::template store<true>(y0 + d * a.y_stride, o);
     });
 }
 

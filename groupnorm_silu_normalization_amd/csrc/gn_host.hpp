@@ -5,8 +5,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
-#include <type_traits>
-#include <vector>
+#include <initializer_list>
 
 #include "gn_types.hpp"
 #include "gnsilu.h"
@@ -80,7 +79,7 @@ struct Call {
     DeviceGuard guard;
 };
 
-inline gn_status begin_call(void *stream, const std::vector<const void *> &ptrs, Call *c) {
+inline gn_status begin_call(void *stream, std::initializer_list<const void *> ptrs, Call *c) {
     c->stream = static_cast<hipStream_t>(stream);
     gn_status st = stream_device(c->stream, &c->dev);
     if (st != GN_OK) return st;

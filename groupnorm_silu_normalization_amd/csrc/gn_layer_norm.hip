@@ -93,10 +93,25 @@ __device__ __forceinline__ void piece_at(const LnArgs &a, int p, int *c, int *lo
     }
 }
 
-// The value of a piece's channel i where it is the lane's own, else 0.  (A lane
-// beyond the row drops its whole sum.)
-template <bool TAIL> __device__ __forceinline__ float own(int i, int lo, float v) {
-    return !TAIL || i >= lo ? v : 0.0f;
+// The calling lane's row slot; a scalar when whole waves share it.
+template <int TPR> __device__ __forceinline__ int row_slot() {
+    const int slot = static_cast<int>(threadIdx.x) / TPR;
+    return TPR >= 64 ? __builtin_amdgcn_readfirstlane(slot) : slot;
+}
+
+// The sum over a piece's own channels of f(i); 0 for a lane beyond the row.
+// edge: wave_has_edge.
+template <int W, bool TAIL, class F>
+__device__ __forceinline__ float own_sum(int lo, bool edge, F &&f) {
+    float p = 0.0f;
+    if (TAIL && edge) {
+#pragma unroll
+        for (int i = 0; i < W; ++i) p += i >= lo ? f(i) : 0.0f;
+        return p;
+    }
+#pragma unroll
+    for (int i = 0; i < W; ++i) p += f(i);
+    return lo < W ? p : 0.0f;
 }
 
 // The rows of a row slot: base + slot, then one grid's worth of rows further,
@@ -145,18 +160,22 @@ __global__ __launch_bounds__(THREADS) void gn_layer_norm(LnArgs a) {
     constexpr int kRed = TPR > 64 ? THREADS / 64 : 1;
     constexpr int kGroup = TPR < kBlock8 / W ? TPR : kBlock8 / W;
     __shared__ float red[2 * kRed];
-    const int t = threadIdx.x % TPR;
+    const int t = threadIdx.x % TPR, slot = row_slot<TPR>();
     const T *x = static_cast<const T *>(a.x);
     T *y = static_cast<T *>(a.y);
     int c[NV], lo[NV];
+    bool edge[NV];
 #pragma unroll
-    for (int j = 0; j < NV; ++j) piece_at<W, TAIL>(a, t + j * TPR, &c[j], &lo[j]);
+    for (int j = 0; j < NV; ++j) {
+        piece_at<W, TAIL>(a, t + j * TPR, &c[j], &lo[j]);
+        edge[j] = wave_has_edge<W, TAIL>(lo[j]);
+    }
     using Row = ForwardRow<D, W, NV>;
     auto fetch = [&](Row &r, int64_t m) {
 #pragma unroll
         for (int j = 0; j < NV; ++j) r.v[j].template load<false>(x + m * a.x_stride + c[j]);
     };
-    RowLoop<Row, kSlots> loop{a.M, static_cast<int>(threadIdx.x / TPR)};
+    RowLoop<Row, kSlots> loop{a.M, slot};
     loop.begin(fetch);
     float ga[NV][W], be[NV][W];
 #pragma unroll
@@ -169,25 +188,17 @@ __global__ __launch_bounds__(THREADS) void gn_layer_norm(LnArgs a) {
     loop.run(fetch, [&](const Row &r, int64_t m, bool live) {
         float s[1] = {0.0f};
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            float p = 0.0f;
-#pragma unroll
-            for (int i = 0; i < W; ++i) p += own<TAIL>(i, lo[j], r.v[j].get(i));
-            s[0] += lo[j] < W ? p : 0.0f;
-        }
+        for (int j = 0; j < NV; ++j)
+            s[0] += own_sum<W, TAIL>(lo[j], edge[j], [&](int i) { return r.v[j].get(i); });
         row_sum<TPR>(s, red);
         const float mean = s[0] / fc;
         float q[1] = {0.0f};
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            float p = 0.0f;
-#pragma unroll
-            for (int i = 0; i < W; ++i) {
-                const float d = own<TAIL>(i, lo[j], r.v[j].get(i) - mean);
-                p = fmaf(d, d, p);
-            }
-            q[0] += lo[j] < W ? p : 0.0f;
-        }
+        for (int j = 0; j < NV; ++j)
+            q[0] += own_sum<W, TAIL>(lo[j], edge[j], [&](int i) {
+                const float d = r.v[j].get(i) - mean;
+                return d * d;
+            });
         row_sum<TPR>(q, red + kRed);
         const float rstd = 1.0f / sqrtf(q[0] / fc + a.eps);
         if (live && t == 0) {
@@ -210,8 +221,8 @@ __global__ __launch_bounds__(THREADS) void gn_layer_norm(LnArgs a) {
             // writes, computed alike.
             Piece<D, W>::template store<SAVE>(y + m * a.y_stride + c[j], o);
             if constexpr (SAVE)
-                store_block8<W, TAIL, true>(block8_encode<W>(f, E), E, a.codes_out, a.scales_out,
-                                            m * a.C, m * nsb, c[j], lo[j]);
+                store_block8<W, TAIL, true>(block8_encode<W>(f, E), E, a.codes_out + m * a.C,
+                                            a.scales_out + m * nsb, c[j], lo[j]);
         }
     });
 }
@@ -223,9 +234,13 @@ template <class D, int W, bool TAIL, int NV, bool SAVED> struct BackwardRow {
     Piece<D, W> vx[SAVED ? 1 : NV], vy[NV];
     Piece8<W, TAIL> v8[SAVED ? NV : 1];
     float mean, rstd;
-    __device__ __forceinline__ void centred(int j, int c, float (&o)[W]) const {  // x - mean
+    // x - mean
+    __device__ __forceinline__ void centred(int j, int c, bool edge, float (&o)[W]) const {
         if constexpr (SAVED) {
-            v8[j].widen_less(c, mean, o);
+            float mu[W];
+#pragma unroll
+            for (int i = 0; i < W; ++i) mu[i] = mean;
+            v8[j].widen_less(c, mu, edge, o);
         } else {
 #pragma unroll
             for (int i = 0; i < W; ++i) o[i] = vx[j].get(i) - mean;
@@ -252,20 +267,25 @@ __global__ __launch_bounds__(THREADS) void gn_layer_norm_backward(LnArgs a) {
     constexpr int kSlots = THREADS / TPR;
     constexpr int kRed = TPR > 64 ? 2 * (THREADS / 64) : 1;
     __shared__ float red[2 * kRed];
-    const int t = threadIdx.x % TPR, slot = threadIdx.x / TPR;
+    const int t = threadIdx.x % TPR, slot = row_slot<TPR>();
     const T *x = static_cast<const T *>(a.x);
     const T *dy = static_cast<const T *>(a.dy);
     T *dx = static_cast<T *>(a.y);
     int c[NV], lo[NV];
+    bool edge[NV];
 #pragma unroll
-    for (int j = 0; j < NV; ++j) piece_at<W, TAIL>(a, t + j * TPR, &c[j], &lo[j]);
+    for (int j = 0; j < NV; ++j) {
+        piece_at<W, TAIL>(a, t + j * TPR, &c[j], &lo[j]);
+        edge[j] = wave_has_edge<W, TAIL>(lo[j]);
+    }
     const int64_t nsb = (a.C + kBlock8 - 1) / kBlock8;
     using Row = BackwardRow<D, W, TAIL, NV, SAVED>;
+    auto at8 = [&](int j) { return Piece8At<W, TAIL>(a.codes, a.scales, 0, a.C, c[j]); };
     auto fetch = [&](Row &r, int64_t m) {
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             if constexpr (SAVED)
-                r.v8[j].load(a.codes, a.scales, m * a.C, m * nsb, c[j]);
+                r.v8[j].load(at8(j), m * a.C, m * nsb);
             else
                 r.vx[j].template load<false>(x + m * a.x_stride + c[j]);
             r.vy[j].template load<false>(dy + m * a.dy_stride + c[j]);
@@ -289,31 +309,24 @@ __global__ __launch_bounds__(THREADS) void gn_layer_norm_backward(LnArgs a) {
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             float x[W];
-            r.centred(j, c[j], x);
-            float p0 = 0.0f, p1 = 0.0f;
+            r.centred(j, c[j], edge[j], x);
+            float g[W];
 #pragma unroll
-            for (int i = 0; i < W; ++i) {
-                const float g = r.vy[j].get(i) * ga[j][i];
-                p0 += own<TAIL>(i, lo[j], g);
-                if constexpr (TAIL)
-                    p1 += own<TAIL>(i, lo[j], g * x[i]);
-                else
-                    p1 = fmaf(g, x[i], p1);
-            }
-            s[0] += lo[j] < W ? p0 : 0.0f;
-            s[1] += lo[j] < W ? p1 : 0.0f;
+            for (int i = 0; i < W; ++i) g[i] = r.vy[j].get(i) * ga[j][i];
+            s[0] += own_sum<W, TAIL>(lo[j], edge[j], [&](int i) { return g[i]; });
+            s[1] += own_sum<W, TAIL>(lo[j], edge[j], [&](int i) { return g[i] * x[i]; });
         }
         row_sum<TPR>(s, red + par * kRed);
         par ^= 1;
         if (!live) return;  // no barrier from here on
-        // The widened values are made again rather than kept across the sums:
-        // a dozen registers fewer, and with them twice the waves.
-        r.opaque();
+        // With two pieces or more the widened values are made again rather than
+        // kept across the sums, for their registers.
+        if constexpr (NV > 1) r.opaque();
         const float s0 = s[0] * a.inv_c, s1 = r.rstd * r.rstd * (s[1] * a.inv_c);
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             float x[W], o[W];
-            r.centred(j, c[j], x);
+            r.centred(j, c[j], edge[j], x);
 #pragma unroll
             for (int i = 0; i < W; ++i) {
                 const float d = r.vy[j].get(i);
@@ -439,7 +452,8 @@ __global__ __launch_bounds__(kColLanes *kColParts) void gn_column_sums(const flo
 // Workgroups: eight waves' worth of lanes per SIMD of 256 CUs forward, four
 // backward, where each workgroup writes a partial row.
 constexpr int64_t kForwardLanes = int64_t{2048} * 256;
-constexpr int64_t kBackwardBlocks = 256;  // one per CU
+constexpr int64_t kBackwardBlocks = 256;  // one per CU, or more when there are
+constexpr int64_t kMaxRun = 4096;         // more rows than a slot should add up in fp32
 
 // Lanes of a row: the fewest (a power of two) that hold it with `nv` pieces
 // each.
@@ -526,7 +540,8 @@ void launch_forward(const LnShape &s, const LnArgs &a, hipStream_t st) {
 }
 
 int64_t backward_blocks(const LnShape &s, int64_t M) {
-    return std::min(ceil_div(M, backward_threads(s.tpr, s.nv) / s.tpr), kBackwardBlocks);
+    const int64_t slots = backward_threads(s.tpr, s.nv) / s.tpr;
+    return std::max(std::min(ceil_div(M, slots), kBackwardBlocks), ceil_div(M, slots * kMaxRun));
 }
 
 template <class D>
@@ -634,6 +649,8 @@ gn_status gn_layer_norm_rows_backward_workspace(int64_t M, int64_t C, int dtype,
     if (bytes_out == nullptr) return GN_INVALID_ARGUMENT;
     const gn_status st = check_ln(M, C, dtype, nullptr, 0, C);
     if (st != GN_OK) return st;
+    if (M > 0 && backward_blocks(ln_shape(C, dtype, false), M) >= int64_t{1} << 22)
+        return GN_UNSUPPORTED;
     *bytes_out = static_cast<int64_t>(backward_workspace(M, C, dtype));
     return GN_OK;
 }
@@ -661,6 +678,8 @@ gn_status gn_layer_norm_rows_backward(const void *dy, int64_t dy_stride, const v
     const bool grads = dgamma != nullptr || dbeta != nullptr;
     if (M == 0 && !grads) return GN_OK;
     const size_t need = grads ? backward_workspace(M, C, dtype) : 0;
+    if (M > 0 && backward_blocks(ln_shape(C, dtype, false), M) >= int64_t{1} << 22)
+        return GN_UNSUPPORTED;  // a dispatch holds fewer than 2^32 work-items
     if (need > 0 && workspace == nullptr) return GN_INVALID_ARGUMENT;
     if (need > 0 && (workspace_bytes < 0 || static_cast<size_t>(workspace_bytes) < need))
         return GN_SCRATCH_TOO_SMALL;

@@ -265,47 +265,63 @@ template <> struct Codes<1> {
 };
 
 // A piece of saved values: its codes and the scale bytes of its first and last
-// channel (different only for a last piece read at C-W; `split` channels of it
-// lie in the first one's block).
+// channel (different only for a last piece read at C-W).
+template <int W, bool TAIL> struct Piece8At {  // where a row's piece at channel c lies
+    const int8_t *q;
+    const uint8_t *e0, *e1;
+    __device__ __forceinline__ Piece8At(const int8_t *codes, const uint8_t *scales, int64_t row,
+                                        int C, int c)
+        : q(codes + row * C + c),
+          e0(scales + row * ((C + kBlock8 - 1) / kBlock8) + c / kBlock8),
+          e1(scales + row * ((C + kBlock8 - 1) / kBlock8) + (c + W - 1) / kBlock8) {}
+};
 template <int W, bool TAIL> struct Piece8 {
     Codes<W> q;
     uint32_t e0, e1;
-    __device__ __forceinline__ void load(const int8_t *codes, const uint8_t *scales, int64_t row_c,
-                                         int64_t row_s, int c) {
-        q.load(codes + row_c + c);
-        e0 = scales[row_s + c / kBlock8];
-        if constexpr (TAIL) e1 = scales[row_s + (c + W - 1) / kBlock8];
+    // `dq` codes and `de` scales further on
+    __device__ __forceinline__ void load(const Piece8At<W, TAIL> &at, int64_t dq, int64_t de) {
+        q.load(at.q + dq);
+        e0 = at.e0[de];
+        if constexpr (TAIL) e1 = at.e1[de];
     }
-    __device__ __forceinline__ void widen(int c, float (&o)[W]) const {
+    // The values less mu, in one fma each.  edge: whether a lane of the wave
+    // holds a last piece read at C-W (wave_has_edge); only that one can lie in
+    // two blocks.
+    __device__ __forceinline__ void widen_less(int c, const float (&mu)[W], bool edge,
+                                               float (&o)[W]) const {
         const float s0 = block8_step(e0);
-        if constexpr (TAIL) {
+        if (TAIL && edge) {
             const float s1 = block8_step(e1);
             const int split = kBlock8 - c % kBlock8;
 #pragma unroll
             for (int j = 0; j < W; ++j)
-                o[j] = static_cast<float>(q.get(j)) * (j < split ? s0 : s1);
+                o[j] = fmaf(static_cast<float>(q.get(j)), j < split ? s0 : s1, -mu[j]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < W; ++j) o[j] = fmaf(static_cast<float>(q.get(j)), s0, -mu[j]);
+        }
+    }
+    __device__ __forceinline__ void widen(int c, bool edge, float (&o)[W]) const {
+        const float s0 = block8_step(e0);
+        if (TAIL && edge) {
+            const float s1 = block8_step(e1);
+            const int split = kBlock8 - c % kBlock8;
+#pragma unroll
+            for (int j = 0; j < W; ++j) o[j] = static_cast<float>(q.get(j)) * (j < split ? s0 : s1);
         } else {
 #pragma unroll
             for (int j = 0; j < W; ++j) o[j] = static_cast<float>(q.get(j)) * s0;
         }
     }
     __device__ __forceinline__ void opaque() { q.opaque(); }
-    __device__ __forceinline__ void widen_less(int c, float mu, float (&o)[W]) const {
-        float m[W];
-#pragma unroll
-        for (int j = 0; j < W; ++j) m[j] = mu;
-        widen_less(c, m, o);
-    }
-    // The values less mu, in one fma each.
-    __device__ __forceinline__ void widen_less(int c, const float (&mu)[W], float (&o)[W]) const {
-        const float s0 = block8_step(e0);
-        const float s1 = TAIL ? block8_step(e1) : 0.0f;
-        const int split = TAIL ? kBlock8 - c % kBlock8 : W;
-#pragma unroll
-        for (int j = 0; j < W; ++j)
-            o[j] = fmaf(static_cast<float>(q.get(j)), TAIL && j >= split ? s1 : s0, -mu[j]);
-    }
 };
+
+// Whether a lane of the wave holds a last piece whose first channels are
+// another piece's (0 < lo < W): the work such a piece needs is left out of the
+// waves that have none.
+template <int W, bool TAIL> __device__ __forceinline__ bool wave_has_edge(int lo) {
+    return TAIL && __builtin_amdgcn_ballot_w64(lo > 0 && lo < W) != 0;
+}
 
 // Which bits of a raw piece count for its block's maximum: the magnitudes of
 // the channels j >= lo.  Cleared words cost nothing, as the signs have to be
@@ -395,13 +411,13 @@ __device__ __forceinline__ Codes<W> block8_encode(const float (&v)[W], uint32_t 
     return q;
 }
 
-// Writes a piece's codes and, from the block's first piece, its scale.
-// c: the piece's first channel in memory; lo: its first own channel.
+// Writes a piece's codes and, from the block's first piece, its scale, into a
+// row's codes and scales.  c: the piece's first channel in memory; lo: its
+// first own channel.
 template <int W, bool TAIL, bool NT>
 __device__ __forceinline__ void store_block8(const Codes<W> &q, uint32_t E, int8_t *codes,
-                                             uint8_t *scales, int64_t row_c, int64_t row_s, int c,
-                                             int lo) {
-    int8_t *p = codes + row_c + c;
+                                             uint8_t *scales, int c, int lo) {
+    int8_t *p = codes + c;
     if (!TAIL || lo == 0) {
         q.template store<NT>(p);
     } else {
@@ -409,7 +425,7 @@ __device__ __forceinline__ void store_block8(const Codes<W> &q, uint32_t E, int8
         for (int j = 0; j < W; ++j)
             if (j >= lo) p[j] = static_cast<int8_t>(q.get(j));
     }
-    if ((c + lo) % kBlock8 == 0) scales[row_s + (c + lo) / kBlock8] = static_cast<uint8_t>(E);
+    if ((c + lo) % kBlock8 == 0) scales[(c + lo) / kBlock8] = static_cast<uint8_t>(E);
 }
 
 }  // namespace gnsilu
