@@ -62,6 +62,12 @@ struct RowArgs {
     int G, Cg;
     Affine af;
     Tiles tl;
+    // pass 2 of several samples: workgroups from `rows_end` on add up dgamma
+    // and dbeta
+    uint32_t rows_end;
+    int64_t N;
+    const float *sums;  // [N][2][C]
+    void *dgamma, *dbeta;
 };
 
 // The calling lane's sample, workgroup of the sample, row slot and piece.
@@ -388,10 +394,10 @@ __global__ __launch_bounds__(kLanes) void gn_grad_groups(FinishArgs a) {
     }
 }
 
-// dgamma and dbeta of N samples (zeros for none).
-__global__ __launch_bounds__(kLanes) void gn_grad_samples(const float *sums, int64_t N, int C,
-                                                          void *dgamma, void *dbeta, int type) {
-    const int c = static_cast<int>(blockIdx.x) * kLanes + static_cast<int>(threadIdx.x);
+// dgamma and dbeta of N samples (zeros for none), 256 channels per workgroup.
+__device__ __forceinline__ void add_samples(const float *sums, int64_t N, int C, int block,
+                                            void *dgamma, void *dbeta, int type) {
+    const int c = block * kLanes + static_cast<int>(threadIdx.x);
     if (c >= C) return;
     double s1 = 0.0, s2 = 0.0;
     for (int64_t n = 0; n < N; ++n) {
@@ -401,6 +407,9 @@ __global__ __launch_bounds__(kLanes) void gn_grad_samples(const float *sums, int
     if (dbeta != nullptr) store_affine(dbeta, type, c, static_cast<float>(s1));
     if (dgamma != nullptr) store_affine(dgamma, type, c, static_cast<float>(s2));
 }
+__global__ __launch_bounds__(kLanes) void gn_grad_zero(int C, void *dgamma, void *dbeta, int type) {
+    add_samples(nullptr, 0, C, static_cast<int>(blockIdx.x), dgamma, dbeta, type);
+}
 
 // Pass 2: dx = dt*scale - (x-mean)*rstd^2*b - rstd*a, from the rows that pass 1
 // read last to those that it read first, so that what the Infinity Cache still
@@ -409,6 +418,11 @@ __global__ __launch_bounds__(kLanes) void gn_grad_samples(const float *sums, int
 template <class D, int W, bool TAIL, bool SILU, bool SAVED>
 __global__ __launch_bounds__(kLanes) void gn_grad_input(RowArgs a) {
     using T = typename D::storage;
+    if (blockIdx.x >= a.rows_end) {
+        add_samples(a.sums, a.N, a.tl.C, static_cast<int>(blockIdx.x - a.rows_end), a.dgamma,
+                    a.dbeta, a.af.type);
+        return;
+    }
     const Tiles &tl = a.tl;
     const Place<W, TAIL> at(tl);
     const int64_t row0 = at.n * tl.L + at.r;
@@ -583,7 +597,7 @@ dim3 grid_of(int64_t N, const Tiles &t) {
 }
 // A dispatch holds fewer than 2^32 work-items.
 bool grid_fits(int64_t N, const Tiles &t, int lanes = kLanes) {
-    const int64_t most = (int64_t{1} << 32) / lanes;
+    const int64_t most = (int64_t{1} << 32) / lanes - GN_MAX_CHANNELS;  // and pass 2's sums
     return N < most && t.K < most && N * t.K < most && N * t.K * t.ncb < most;
 }
 
@@ -794,11 +808,10 @@ gn_status gn_silu_rows_backward(const void *dy, const void *x, const void *codes
                      empty ? nullptr : workspace},
                     &c);
     if (st != GN_OK) return st;
-    const dim3 sgrid(static_cast<unsigned>(ceil_div(C, kLanes)));
     const int atype = affine_type(dtype);
     if (empty) {
-        gn_grad_samples<<<sgrid, kLanes, 0, c.stream>>>(nullptr, 0, static_cast<int>(C), dgamma,
-                                                        dbeta, atype);
+        gn_grad_zero<<<dim3(static_cast<unsigned>(ceil_div(C, kLanes))), kLanes, 0, c.stream>>>(
+            static_cast<int>(C), dgamma, dbeta, atype);
         return finish_launch();
     }
     float *ws = static_cast<float *>(workspace);
@@ -832,6 +845,10 @@ gn_status gn_silu_rows_backward(const void *dy, const void *x, const void *codes
     f.af = a.af;
     f.coef = a.Cg <= 64 ? coef : nullptr;
     a.coef = coef;
+    a.N = N;
+    a.sums = f.sums;
+    a.dgamma = dgamma;
+    a.dbeta = dbeta;
     with_pieces(C, dtype, [&](auto d, auto wc, auto tail) {
         using D = decltype(d);
         constexpr int W = decltype(wc)::value;
@@ -854,8 +871,10 @@ gn_status gn_silu_rows_backward(const void *dy, const void *x, const void *codes
                 gn_grad_groups<<<dim3(static_cast<unsigned>(N * G)), kLanes, 0, c.stream>>>(g);
             }
             a.tl = p.input;
-            gn_grad_input<D, W, TAIL, SILU, SAVED>
-                <<<grid_of(N, a.tl), kLanes, 0, c.stream>>>(a);
+            dim3 grid = grid_of(N, a.tl);
+            a.rows_end = grid.x;
+            if (grads && N > 1) grid.x += static_cast<unsigned>(ceil_div(C, kLanes));
+            gn_grad_input<D, W, TAIL, SILU, SAVED><<<grid, kLanes, 0, c.stream>>>(a);
         };
         auto by_saved = [&](auto silu) {
             if (codes != nullptr)
@@ -868,8 +887,6 @@ gn_status gn_silu_rows_backward(const void *dy, const void *x, const void *codes
         else
             by_saved(IC<0>{});
     });
-    if (grads && N > 1)
-        gn_grad_samples<<<sgrid, kLanes, 0, c.stream>>>(f.sums, N, f.C, dgamma, dbeta, atype);
     return finish_launch();
 }
 
