@@ -114,11 +114,13 @@ __device__ __forceinline__ float own_sum(int lo, bool edge, F &&f) {
     return lo < W ? p : 0.0f;
 }
 
-// The rows of a row slot: base + slot, then one grid's worth of rows further,
-// each row's loads issued before the row ahead of it is worked on.  Slots
-// behind the last row read that row and do not store (the loop's end is the
-// same for the whole workgroup, which has barriers in it).
-template <class Row, int SLOTS> struct RowLoop {
+// The rows of a row slot: base + slot, then one grid's worth of rows further.
+// AHEAD: each row's loads are issued before the row ahead of it is worked on
+// (not where a lane's four pieces of fp32 leave no registers for them: the
+// backward pass at (2796,12000) took 187 us with them spilt, 87 without).
+// Slots behind the last row read that row and do not store (the loop's end is
+// the same for the whole workgroup, which has barriers in it).
+template <class Row, int SLOTS, bool AHEAD> struct RowLoop {
     int64_t M;
     int slot;
     Row a, b;
@@ -133,6 +135,13 @@ template <class Row, int SLOTS> struct RowLoop {
         const int64_t step = int64_t{gridDim.x} * SLOTS;
         for (int64_t base = int64_t{blockIdx.x} * SLOTS;;) {
             int64_t next = base + step;
+            if constexpr (!AHEAD) {
+                work(a, row(base), base + slot < M);
+                if (next >= M) break;
+                base = next;
+                fetch(a, row(base));
+                continue;
+            }
             if (next < M) fetch(b, row(next));
             work(a, row(base), base + slot < M);
             if (next >= M) break;
@@ -175,7 +184,7 @@ __global__ __launch_bounds__(THREADS) void gn_layer_norm(LnArgs a) {
 #pragma unroll
         for (int j = 0; j < NV; ++j) r.v[j].template load<false>(x + m * a.x_stride + c[j]);
     };
-    RowLoop<Row, kSlots> loop{a.M, slot};
+    RowLoop<Row, kSlots, sizeof(T) == 2 || NV < 4> loop{a.M, slot};
     loop.begin(fetch);
     float ga[NV][W], be[NV][W];
 #pragma unroll
@@ -293,7 +302,7 @@ __global__ __launch_bounds__(THREADS) void gn_layer_norm_backward(LnArgs a) {
         r.mean = a.mean[m];
         r.rstd = a.rstd[m];
     };
-    RowLoop<Row, kSlots> loop{a.M, slot};
+    RowLoop<Row, kSlots, sizeof(T) == 2 || NV < 4> loop{a.M, slot};
     loop.begin(fetch);
     float ga[NV][W], dg[NV][W], db[NV][W];
 #pragma unroll

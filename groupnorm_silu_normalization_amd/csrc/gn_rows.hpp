@@ -351,12 +351,14 @@ __device__ __forceinline__ uint32_t max2_u16(uint32_t a, uint32_t b) {
 }
 
 // The scale byte of the block that the calling lane's piece belongs to; the
-// block's pieces are held by GROUP consecutive, aligned lanes (all of which
-// call this).  Magnitudes of every type order like their bits, so the maxima
+// block's pieces are held by GROUP consecutive, aligned lanes -- or, where rows
+// are that short, by `group` of them, a smaller power of two, the same for all
+// lanes -- all of which call this.  Magnitudes of every type order like their bits, so the maxima
 // are taken on the raw words, two 16-bit values at a time.
 template <class D, int W, int GROUP>
 __device__ __forceinline__ uint32_t block8_exponent(const Piece<D, W> &v,
-                                                    const Magnitudes<D, W> &mag) {
+                                                    const Magnitudes<D, W> &mag,
+                                                    int group = GROUP) {
     uint32_t top;
     if constexpr (W == 8) {
         top = max2_u16(max2_u16(v.w[0] & mag.m[0], v.w[1] & mag.m[1]),
@@ -375,7 +377,12 @@ __device__ __forceinline__ uint32_t block8_exponent(const Piece<D, W> &v,
     } else {
         top = __float_as_uint(v.b) & mag.m[0];
     }
-    top = lane_max<GROUP>(top);
+    if (group >= GROUP) {
+        top = lane_max<GROUP>(top);
+    } else if (group >= 2) {  // rows of fewer lanes
+        top = lane_max<2>(top);
+        if (group >= 4) top = max(top, dpp<kDppXor2>(top));
+    }
     if constexpr (std::is_same<D, Bf16>::value)
         return top >> 7;
     else if constexpr (std::is_same<D, Fp16>::value)
