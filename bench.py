@@ -63,6 +63,7 @@ H200_US = {                        # the pages' new-kernel column (H200), contex
 HEADLINE = 3                       # index into gn_inputs.WORKLOADS
 TRAFFIC_FILE = os.path.join(ROOT, "profiles", "traffic_gn_silu_1x256x1024x1024.json")
 KERNEL_SOURCES = [
+    os.path.join(ROOT, "groupnorm_silu_normalization_amd", "csrc", "gn_types.hpp"),
     os.path.join(ROOT, "groupnorm_silu_normalization_amd", "csrc", "gn_kernels.hpp"),
     os.path.join(ROOT, "groupnorm_silu_normalization_amd", "csrc", "gn_api.hip"),
     os.path.join(ROOT, "groupnorm_silu_normalization_amd", "csrc", "gn_conv.hpp"),
