@@ -681,7 +681,8 @@ def layer_norm_rows_backward(dy, x, mean, rstd, weight=None, *, weight_grad=True
         size = _workspace_bytes("gn_layer_norm_rows_backward_workspace", M, C, dtype)
         if size is None:
             return None
-        ws = torch.empty(size, dtype=torch.uint8, device=dy.device)
+        if size:
+            ws = torch.empty(size, dtype=torch.uint8, device=dy.device)
     code = _run(
         lib.gn_layer_norm_rows_backward, dy, _addr(dy), step, xp, xstep, codes, scales,
         _addr(mean), _addr(rstd), _addr(weight), _addr(out), ostep, _addr(dw), _addr(db), M, C,

@@ -45,6 +45,8 @@ struct LnArgs {
     uint8_t *scales_out;
     float *mean, *rstd;     // [M]; forward: written unless null, backward: read
     float *part;            // backward: [2][blocks][C] partial dgamma, dbeta, or null
+    uint32_t rows_end;      // backward of few rows: workgroups from here on take columns
+    void *dgamma, *dbeta;   // (those workgroups' results)
     int64_t M, x_stride, dy_stride, y_stride;
     int C, P;
     float eps, inv_c;       // inv_c: 1 / C
@@ -123,6 +125,7 @@ __device__ __forceinline__ float own_sum(int lo, bool edge, F &&f) {
 template <class Row, int SLOTS, bool AHEAD> struct RowLoop {
     int64_t M;
     int slot;
+    uint32_t blocks;  // workgroups that share the rows
     Row a, b;
     __device__ __forceinline__ int64_t row(int64_t base) const {
         return base + slot < M ? base + slot : M - 1;
@@ -132,7 +135,7 @@ template <class Row, int SLOTS, bool AHEAD> struct RowLoop {
     }
     template <class Fetch, class Work>
     __device__ __forceinline__ void run(Fetch &&fetch, Work &&work) {
-        const int64_t step = int64_t{gridDim.x} * SLOTS;
+        const int64_t step = int64_t{blocks} * SLOTS;
         for (int64_t base = int64_t{blockIdx.x} * SLOTS;;) {
             int64_t next = base + step;
             if constexpr (!AHEAD) {
@@ -184,7 +187,7 @@ __global__ __launch_bounds__(THREADS) void gn_layer_norm(LnArgs a) {
 #pragma unroll
         for (int j = 0; j < NV; ++j) r.v[j].template load<false>(x + m * a.x_stride + c[j]);
     };
-    RowLoop<Row, kSlots, sizeof(T) == 2 || NV < 4> loop{a.M, slot};
+    RowLoop<Row, kSlots, sizeof(T) == 2 || NV < 4> loop{a.M, slot, gridDim.x};
     loop.begin(fetch);
     float ga[NV][W], be[NV][W];
 #pragma unroll
@@ -270,10 +273,91 @@ template <class D, int W, bool TAIL, int NV, bool SAVED> struct BackwardRow {
     }
 };
 
-template <class D, int W, bool TAIL, int TPR, int NV, int THREADS, bool SAVED>
+// dgamma and dbeta of 16 pieces' channels over all rows, by a workgroup of
+// THREADS lanes: THREADS / 16 row slots, four rows' loads of a slot in flight;
+// the slots of a wave by a butterfly, then the waves in order.
+constexpr int kColPieces = 16;
+template <class D, int W, bool TAIL, int THREADS, bool SAVED>
+__device__ __forceinline__ void few_rows_columns(const LnArgs &a, int block) {
+    using T = typename D::storage;
+    constexpr int kSlots = THREADS / kColPieces, kWaves = THREADS / 64, kBatch = 4;
+    __shared__ float red[2][kWaves][kColPieces * W];
+    const int t = threadIdx.x % kColPieces, slot = threadIdx.x / kColPieces;
+    int c, lo;
+    piece_at<W, TAIL>(a, block * kColPieces + t, &c, &lo);
+    const bool edge = SAVED && wave_has_edge<W, TAIL>(lo);
+    const int64_t nsb = (a.C + kBlock8 - 1) / kBlock8;
+    const T *x = static_cast<const T *>(a.x);
+    const T *dy = static_cast<const T *>(a.dy);
+    using Row = BackwardRow<D, W, TAIL, 1, SAVED>;
+    float g[W], b[W];
+#pragma unroll
+    for (int i = 0; i < W; ++i) g[i] = b[i] = 0.0f;
+    for (int64_t base = slot; base < a.M; base += kBatch * kSlots) {
+        Row r[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const int64_t m = base + u * kSlots < a.M ? base + u * kSlots : a.M - 1;
+            if constexpr (SAVED)
+                r[u].v8[0].load(Piece8At<W, TAIL>(a.codes, a.scales, 0, a.C, c), m * a.C, m * nsb);
+            else
+                r[u].vx[0].template load<false>(x + m * a.x_stride + c);
+            r[u].vy[0].template load<false>(dy + m * a.dy_stride + c);
+            r[u].mean = a.mean[m];
+            r[u].rstd = a.rstd[m];
+        }
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            if (base + u * kSlots >= a.M) break;
+            float v[W];
+            r[u].centred(0, c, edge, v);
+#pragma unroll
+            for (int i = 0; i < W; ++i) {
+                const float d = r[u].vy[0].get(i);
+                g[i] = fmaf(d * r[u].rstd, v[i], g[i]);
+                b[i] += d;
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+#pragma unroll
+        for (int o = kColPieces; o < 64; o <<= 1) {
+            g[i] += __shfl_xor(g[i], o, 64);
+            b[i] += __shfl_xor(b[i], o, 64);
+        }
+        if ((threadIdx.x & 63) < kColPieces) {
+            red[0][threadIdx.x >> 6][t * W + i] = g[i];
+            red[1][threadIdx.x >> 6][t * W + i] = b[i];
+        }
+    }
+    __syncthreads();
+    // thread (which, piece, channel)
+    const int e = threadIdx.x % (kColPieces * W), which = threadIdx.x / (kColPieces * W);
+    if (which >= 2) return;
+    piece_at<W, TAIL>(a, block * kColPieces + e / W, &c, &lo);
+    void *out = which == 0 ? a.dgamma : a.dbeta;
+    if (out == nullptr || e % W < lo) return;
+    float s = red[which][0][e];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) s += red[which][w][e];
+    store_affine(out, a.af.type, c + e % W, s);
+}
+
+// FEW: few rows.  Workgroups up to rows_end make dx alone, the others dgamma
+// and dbeta from x and dy again: one launch and no partial rows, and what is
+// read twice comes from a cache.
+template <class D, int W, bool TAIL, int TPR, int NV, int THREADS, bool SAVED, bool FEW>
 __global__ __launch_bounds__(THREADS) void gn_layer_norm_backward(LnArgs a) {
     using T = typename D::storage;
     constexpr int kSlots = THREADS / TPR;
+    if constexpr (FEW) {
+        if (blockIdx.x >= a.rows_end) {
+            few_rows_columns<D, W, TAIL, THREADS, SAVED>(
+                a, static_cast<int>(blockIdx.x - a.rows_end));
+            return;
+        }
+    }
     constexpr int kRed = TPR > 64 ? 2 * (THREADS / 64) : 1;
     __shared__ float red[2 * kRed];
     const int t = threadIdx.x % TPR, slot = row_slot<TPR>();
@@ -302,7 +386,7 @@ __global__ __launch_bounds__(THREADS) void gn_layer_norm_backward(LnArgs a) {
         r.mean = a.mean[m];
         r.rstd = a.rstd[m];
     };
-    RowLoop<Row, kSlots, sizeof(T) == 2 || NV < 4> loop{a.M, slot};
+    RowLoop<Row, kSlots, sizeof(T) == 2 || NV < 4> loop{a.M, slot, FEW ? a.rows_end : gridDim.x};
     loop.begin(fetch);
     float ga[NV][W], dg[NV][W], db[NV][W];
 #pragma unroll
@@ -340,13 +424,15 @@ __global__ __launch_bounds__(THREADS) void gn_layer_norm_backward(LnArgs a) {
             for (int i = 0; i < W; ++i) {
                 const float d = r.vy[j].get(i);
                 o[i] = r.rstd * fmaf(-x[i], s1, fmaf(d, ga[j][i], -s0));
-                dg[j][i] = fmaf(d * r.rstd, x[i], dg[j][i]);
-                db[j][i] += d;
+                if constexpr (!FEW) {
+                    dg[j][i] = fmaf(d * r.rstd, x[i], dg[j][i]);
+                    db[j][i] += d;
+                }
             }
             if (lo[j] < W) Piece<D, W>::template store<true>(dx + m * a.y_stride + c[j], o);
         }
     });
-    if (a.part == nullptr) return;
+    if (FEW || a.part == nullptr) return;
     // The row slots of the workgroup: within a wave by butterflies over the
     // lanes that hold the same channels, then slot by slot (wave by wave)
     // through LDS.
@@ -553,18 +639,41 @@ int64_t backward_blocks(const LnShape &s, int64_t M) {
     return std::max(std::min(ceil_div(M, slots), kBackwardBlocks), ceil_div(M, slots * kMaxRun));
 }
 
+// Up to this many rows the columns' workgroups read x and dy again instead of
+// adding up partial rows.
+constexpr int64_t kFewRows = 1024;
+
 template <class D>
-void launch_backward(const LnShape &s, const LnArgs &a, hipStream_t st) {
+void launch_backward(const LnShape &s, LnArgs a, bool grads, hipStream_t st) {
     const int64_t blocks = backward_blocks(s, a.M);
+    const bool few = a.M <= kFewRows;
+    a.rows_end = static_cast<uint32_t>(blocks);
     with_ln_shape<D, false>(s, [&](auto w, auto tail, auto tpr, auto nv) {
         constexpr int W = decltype(w)::value, TPR = decltype(tpr)::value;
         constexpr int NV = decltype(nv)::value, NT = backward_threads(TPR, NV);
         constexpr bool TAIL = decltype(tail)::value != 0;
-        const dim3 grid(static_cast<unsigned>(blocks)), block(NT);
+        const unsigned rows = static_cast<unsigned>(blocks);
+        const unsigned cols =
+            few && grads ? static_cast<unsigned>(ceil_div(s.P, kColPieces)) : 0u;
+        auto launch = [&](auto saved, auto fewc, unsigned grid) {
+            gn_layer_norm_backward<D, W, TAIL, TPR, NV, NT, decltype(saved)::value != 0,
+                                   decltype(fewc)::value != 0><<<grid, NT, 0, st>>>(a);
+        };
+        auto go = [&](auto saved) {
+            if (!few) return launch(saved, IC<0>{}, rows);
+            if (cols > 0 && (a.y == a.x || a.y == a.dy)) {
+                // in place: the columns before any row is overwritten
+                a.rows_end = 0;
+                launch(saved, IC<1>{}, cols);
+                a.rows_end = rows;
+                return launch(saved, IC<1>{}, rows);
+            }
+            launch(saved, IC<1>{}, rows + cols);
+        };
         if (a.codes != nullptr)
-            gn_layer_norm_backward<D, W, TAIL, TPR, NV, NT, true><<<grid, block, 0, st>>>(a);
+            go(IC<1>{});
         else
-            gn_layer_norm_backward<D, W, TAIL, TPR, NV, NT, false><<<grid, block, 0, st>>>(a);
+            go(IC<0>{});
     });
 }
 
@@ -603,7 +712,7 @@ gn_status check_ln(int64_t M, int64_t C, int dtype, const int64_t *in_strides, i
 }
 
 size_t backward_workspace(int64_t M, int64_t C, int dtype) {
-    if (M == 0) return 0;
+    if (M <= kFewRows) return 0;
     return sizeof(float) * 2 * static_cast<size_t>(backward_blocks(ln_shape(C, dtype, false), M)) *
            static_cast<size_t>(C);
 }
@@ -707,7 +816,9 @@ gn_status gn_layer_norm_rows_backward(const void *dy, int64_t dy_stride, const v
     a.y = dx;
     a.mean = const_cast<float *>(mean);
     a.rstd = const_cast<float *>(rstd);
-    a.part = grads ? static_cast<float *>(workspace) : nullptr;
+    a.part = need > 0 ? static_cast<float *>(workspace) : nullptr;
+    a.dgamma = dgamma;
+    a.dbeta = dbeta;
     a.M = M;
     a.x_stride = x_stride;
     a.dy_stride = dy_stride;
@@ -716,10 +827,11 @@ gn_status gn_layer_norm_rows_backward(const void *dy, int64_t dy_stride, const v
     a.P = s.P;
     a.inv_c = 1.0f / static_cast<float>(C);
     a.af = Affine{gamma, nullptr, affine_type(dtype)};
-    if (M > 0) by_type(dtype, [&](auto d) { launch_backward<decltype(d)>(s, a, c.stream); });
-    if (grads)
+    if (M > 0)
+        by_type(dtype, [&](auto d) { launch_backward<decltype(d)>(s, a, grads, c.stream); });
+    if (need > 0 || M == 0)  // M = 0: zeros
         gn_column_sums<<<dim3(static_cast<unsigned>(ceil_div(C, kColLanes)), 2),
-                         kColLanes * kColParts, 0, c.stream>>>(static_cast<const float *>(workspace),
+                         kColLanes * kColParts, 0, c.stream>>>(a.part,
                                      M > 0 ? backward_blocks(s, M) : 0, a.C, dgamma, dbeta,
                                      a.af.type);
     return finish_launch();
