@@ -767,7 +767,7 @@ def group_norm_silu_rows_backward(dy, x, mean, rstd, weight=None, bias=None, app
     size = _workspace_bytes("gn_silu_rows_backward_workspace", N, L, C, G, dtype)
     if size is None:
         return None
-    ws = torch.empty(size, dtype=torch.uint8, device=dy.device)
+    ws = torch.empty(size, dtype=torch.uint8, device=dy.device) if size else None
     code = _run(
         lib.gn_silu_rows_backward, dy, _addr(dy), xp, codes, scales, _addr(mean), _addr(rstd),
         _addr(weight), _addr(bias), _addr(out), _addr(dw), _addr(db), N, L, C, G,

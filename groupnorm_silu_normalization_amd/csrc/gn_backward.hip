@@ -407,8 +407,9 @@ __device__ __forceinline__ void add_samples(const float *sums, int64_t N, int C,
     if (dbeta != nullptr) store_affine(dbeta, type, c, static_cast<float>(s1));
     if (dgamma != nullptr) store_affine(dgamma, type, c, static_cast<float>(s2));
 }
-__global__ __launch_bounds__(kLanes) void gn_grad_zero(int C, void *dgamma, void *dbeta, int type) {
-    add_samples(nullptr, 0, C, static_cast<int>(blockIdx.x), dgamma, dbeta, type);
+__global__ __launch_bounds__(kLanes) void gn_grad_samples(const float *sums, int64_t N, int C,
+                                                          void *dgamma, void *dbeta, int type) {
+    add_samples(sums, N, C, static_cast<int>(blockIdx.x), dgamma, dbeta, type);
 }
 
 // Pass 2: dx = dt*scale - (x-mean)*rstd^2*b - rstd*a, from the rows that pass 1
@@ -459,6 +460,168 @@ __global__ __launch_bounds__(kLanes) void gn_grad_input(RowArgs a) {
         else
             store_from<D, W>(p, o, at.lo);
     });
+}
+
+// The whole backward pass in one launch, for samples small enough: a workgroup
+// takes a strip of whole groups of one sample (strip_c channels, P pieces of
+// a row, a power of two) and holds its x and dy in registers, NP pieces each
+// per lane, so both are read once.  Its channels' sums: the lanes of a wave
+// that hold the same piece by a butterfly, then the waves in order.
+constexpr int kStripLanes = 1024;
+constexpr int kStripMaxPieces = 4;  // NP
+constexpr int kStripMaxRow = 32;    // P
+struct StripArgs {
+    RowArgs r;      // tl.L and tl.C; sums: [N][2][C] to write, or null
+    float *sums;
+    int P, shift;   // pieces of a strip's row, log2
+    int strips;     // per sample
+    double inv_m;
+};
+
+// v plus its value in the lane whose number differs in the bits >= P of 63;
+// P a power of two, the same for all lanes.  (A rotation by 8 within 16 lanes
+// exchanges the halves; after it one by 4 exchanges the quads.)
+__device__ __forceinline__ float fold_from(float v, int P) {
+    auto add = [&](uint32_t o) { v += __uint_as_float(o); };
+    if (P <= 1) add(dpp<kDppXor1>(__float_as_uint(v)));
+    if (P <= 2) add(dpp<kDppXor2>(__float_as_uint(v)));
+    if (P <= 8) add(dpp<kDppRor8>(__float_as_uint(v)));
+    if (P <= 4) add(dpp<kDppRor4>(__float_as_uint(v)));
+    if (P <= 16) {
+        const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v),
+                                                        false, false);
+        v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    }
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false,
+                                                    false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+template <class D, int W, bool SILU, bool SAVED, int NP>
+__global__ __launch_bounds__(kStripLanes) void gn_grad_strip(StripArgs sa) {
+    using T = typename D::storage;
+    constexpr int kWaves = kStripLanes / 64;
+    const RowArgs &a = sa.r;
+    __shared__ float red[2][kWaves][kStripMaxRow * W];
+    __shared__ float coef[2][W];  // a and b of the strip's groups
+    const int tid = threadIdx.x;
+    const int64_t n = blockIdx.x / static_cast<uint32_t>(sa.strips);
+    const int strip = static_cast<int>(blockIdx.x % static_cast<uint32_t>(sa.strips));
+    const int pc = tid & (sa.P - 1), r = tid >> sa.shift, R = kStripLanes >> sa.shift;
+    const int c0 = strip * sa.P * W, c = c0 + pc * W, wide = sa.P * W;
+    const int64_t row0 = n * a.tl.L;
+    using V = Pair<D, W, false, SAVED>;
+    const typename V::From from(a, row0, c);
+    V v[NP];
+#pragma unroll
+    for (int u = 0; u < NP; ++u) {
+        const int64_t l = r + int64_t{u} * R;
+        v[u].load(from, l < a.tl.L ? l : a.tl.L - 1);
+    }
+    Channels<W> ch;
+    ch.load(a, n, c);
+    float s1[W], s2[W];
+#pragma unroll
+    for (int i = 0; i < W; ++i) s1[i] = s2[i] = 0.0f;
+    auto gradient = [&](const V &p, float (&x)[W], float (&g)[W]) {
+        p.centred(c, ch.mu, false, x);
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            g[i] = p.vy.get(i);
+            if constexpr (SILU) g[i] = silu_grad(fmaf(x[i], ch.sc[i], ch.be[i]), g[i]);
+        }
+    };
+#pragma unroll
+    for (int u = 0; u < NP; ++u) {
+        if (r + int64_t{u} * R >= a.tl.L) break;
+        float x[W], g[W];
+        gradient(v[u], x, g);
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            s1[i] += g[i];
+            s2[i] = fmaf(g[i], x[i], s2[i]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+        s1[i] = fold_from(s1[i], sa.P);
+        s2[i] = fold_from(s2[i], sa.P);
+    }
+    if ((tid & 63) < sa.P) {
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            red[0][tid >> 6][pc * W + i] = s1[i];
+            red[1][tid >> 6][pc * W + i] = s2[i];
+        }
+    }
+    __syncthreads();
+    if (tid < wide) {  // one channel each
+        float t1 = red[0][0][tid], t2 = red[1][0][tid];
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w) {
+            t1 += red[0][w][tid];
+            t2 += red[1][w][tid];
+        }
+        const int cc = c0 + tid;
+        t2 *= a.rstd[n * a.G + cc / a.Cg];
+        if (sa.sums != nullptr) {
+            sa.sums[n * 2 * a.tl.C + cc] = t1;
+            sa.sums[n * 2 * a.tl.C + a.tl.C + cc] = t2;
+        } else {
+            if (a.dbeta != nullptr) store_affine(a.dbeta, a.af.type, cc, t1);
+            if (a.dgamma != nullptr) store_affine(a.dgamma, a.af.type, cc, t2);
+        }
+        float ga[1];
+        load_affine<1>(a.af.gamma, a.af.type, cc, 1.0f, ga);
+        red[0][0][tid] = t1 * ga[0];
+        red[1][0][tid] = t2 * ga[0];
+    }
+    __syncthreads();
+    // the groups' sums, in fp64: one group of `wide` channels, or several of a
+    // single piece
+    const int groups = wide / a.Cg;
+    if (tid < 64) {
+        double ta = 0.0, tb = 0.0;
+        if (groups == 1) {
+            for (int e = tid; e < wide; e += 64) {
+                ta += static_cast<double>(red[0][0][e]);
+                tb += static_cast<double>(red[1][0][e]);
+            }
+#pragma unroll
+            for (int o = 1; o < 64; o <<= 1) {
+                ta += __shfl_xor(ta, o, 64);
+                tb += __shfl_xor(tb, o, 64);
+            }
+        } else if (tid < groups) {
+            for (int e = tid * a.Cg; e < (tid + 1) * a.Cg; ++e) {
+                ta += static_cast<double>(red[0][0][e]);
+                tb += static_cast<double>(red[1][0][e]);
+            }
+        }
+        if (tid < groups) {
+            coef[0][tid] = static_cast<float>(ta * sa.inv_m);
+            coef[1][tid] = static_cast<float>(tb * sa.inv_m);
+        }
+    }
+    __syncthreads();
+    float k0[W], k1[W];
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+        const int g = groups == 1 ? 0 : i / a.Cg;
+        k0[i] = -ch.rs[i] * coef[0][g];
+        k1[i] = -ch.rs[i] * ch.rs[i] * coef[1][g];
+    }
+    T *dx = static_cast<T *>(a.y) + row0 * a.tl.C + c;
+#pragma unroll
+    for (int u = 0; u < NP; ++u) {
+        const int64_t l = r + int64_t{u} * R;
+        if (l >= a.tl.L) break;
+        float x[W], g[W], o[W];
+        gradient(v[u], x, g);
+#pragma unroll
+        for (int i = 0; i < W; ++i) o[i] = fmaf(g[i], ch.sc[i], fmaf(x[i], k1[i], k0[i]));
+        Piece<D, W>::template store<true>(dx + l * a.tl.C, o);
+    }
 }
 
 // The apply step that also saves x (kApply, kApplySilu), or x saved alone
@@ -638,15 +801,50 @@ gn_status check_group_rows(int64_t N, int64_t L, int64_t C, int64_t G, int apply
     return GN_OK;
 }
 
+// The single launch: rows of whole pieces, groups of a power of two channels,
+// a strip's rows within kStripMaxPieces pieces per lane, at most
+// kStripMaxBlocks workgroups, and x at most kStripMaxBytes, counted as the
+// 128-byte lines that a strip's rows lie in (a strip of one piece fetches eight
+// times what it uses).  Measured on MI355X, bf16, G = 32 (us a call, single
+// launch / three): (1,256,512) 18/26, (1,4096,128) 22.7/26, (2,4096,128)
+// 25.5/25.5, (8,4096,128) 39/27, (4,2048,512) 26.6/26.2, (8,2048,512) 42/33,
+// (8,1024,1024) 27/34, (8,128,8192) 25/53.
+constexpr int64_t kStripMaxBlocks = 256;
+constexpr int64_t kStripMaxBytes = int64_t{32} << 20;
+struct StripPlan {
+    int P = 0, shift = 0, np = 0, strips = 0;  // np = 0: not taken
+};
+StripPlan strip_plan(int64_t N, int64_t L, int64_t C, int64_t G, int w) {
+    StripPlan s;
+    const int64_t cg = C / G;
+    if (w == 1 || C % w != 0 || (cg & (cg - 1)) != 0) return s;
+    const int64_t wide = std::max<int64_t>(cg, w);
+    if (wide / w > kStripMaxRow || N * (C / wide) > kStripMaxBlocks) return s;
+    s.P = static_cast<int>(wide / w);
+    while ((1 << s.shift) < s.P) ++s.shift;
+    const int64_t np = ceil_div(L, kStripLanes / s.P);
+    if (np > kStripMaxPieces) return s;
+    if (N * L * C * (16 / w) * std::max(1, 8 / s.P) > kStripMaxBytes) return s;
+    s.np = np <= 1 ? 1 : (np <= 2 ? 2 : 4);
+    s.strips = static_cast<int>(C / wide);
+    return s;
+}
+
 struct BackwardPlan {
+    StripPlan strip;
     Tiles sums, input;
     int lanes;  // of pass 1's workgroups
     int tile_c, tiles, width;
     size_t part, total;  // floats
 };
 BackwardPlan backward_plan(int64_t N, int64_t L, int64_t C, int64_t G, int dtype, bool saved) {
-    BackwardPlan p;
+    BackwardPlan p{};
     const int w = piece_width(C, dtype);
+    p.strip = strip_plan(N, L, C, G, w);
+    if (p.strip.np > 0) {
+        p.total = N > 1 ? static_cast<size_t>(N) * 2 * C : 0;
+        return p;
+    }
     p.lanes = N * L * C * elem_bytes(dtype) <= kSmallBytes ? kLanes : kSumLanes;
     p.sums = make_tiles(N, L, C, w, 1, kSumBlocks, kMaxRun, p.lanes);
     p.input = make_tiles(N, L, C, w, 1, kStreamBlocks, 0, kLanes,
@@ -661,8 +859,35 @@ BackwardPlan backward_plan(int64_t N, int64_t L, int64_t C, int64_t G, int dtype
     return p;
 }
 bool backward_fits(int64_t N, const BackwardPlan &p) {
+    if (p.strip.np > 0) return true;
     return grid_fits(N, p.sums, p.lanes) && grid_fits(N, p.input) && N * p.tiles < (int64_t{1} << 22) &&
            N * p.sums.C < (int64_t{1} << 40);
+}
+
+void launch_strip(const StripArgs &sa, unsigned grid, int np, bool silu, bool saved, int dtype,
+                  hipStream_t st) {
+    auto by_np = [&](auto d, auto siluc, auto savedc) {
+        using D = decltype(d);
+        constexpr int W = static_cast<int>(16 / sizeof(typename D::storage));
+        constexpr bool SILU = decltype(siluc)::value != 0, SAVED = decltype(savedc)::value != 0;
+        if (np == 1)
+            gn_grad_strip<D, W, SILU, SAVED, 1><<<grid, kStripLanes, 0, st>>>(sa);
+        else if (np == 2)
+            gn_grad_strip<D, W, SILU, SAVED, 2><<<grid, kStripLanes, 0, st>>>(sa);
+        else
+            gn_grad_strip<D, W, SILU, SAVED, 4><<<grid, kStripLanes, 0, st>>>(sa);
+    };
+    auto by_flags = [&](auto d) {
+        if (silu)
+            saved ? by_np(d, IC<1>{}, IC<1>{}) : by_np(d, IC<1>{}, IC<0>{});
+        else
+            saved ? by_np(d, IC<0>{}, IC<1>{}) : by_np(d, IC<0>{}, IC<0>{});
+    };
+    switch (x_dtype(dtype)) {
+        case GN_DTYPE_F16: by_flags(Fp16{}); break;
+        case GN_DTYPE_F32: by_flags(F32{}); break;
+        default: by_flags(Bf16{}); break;
+    }
 }
 
 // Row forms with a stride (the checkpoints).
@@ -820,20 +1045,21 @@ gn_status gn_silu_rows_backward(const void *dy, const void *x, const void *codes
     if (!empty) {
         p = backward_plan(N, L, C, G, dtype, codes != nullptr);
         if (!backward_fits(N, p)) return GN_UNSUPPORTED;
-        if (workspace == nullptr) return GN_INVALID_ARGUMENT;
+        if (p.total > 0 && workspace == nullptr) return GN_INVALID_ARGUMENT;
         if (workspace_bytes < 0 || static_cast<size_t>(workspace_bytes) < sizeof(float) * p.total)
             return GN_SCRATCH_TOO_SMALL;
     }
     Call c;
     st = begin_call(stream,
                     {dy, x, codes, scales, mean, rstd, gamma, beta, dx, dgamma, dbeta,
-                     empty ? nullptr : workspace},
+                     p.total > 0 ? workspace : nullptr},
                     &c);
     if (st != GN_OK) return st;
+    const dim3 sgrid(static_cast<unsigned>(ceil_div(C, kLanes)));
     const int atype = affine_type(dtype);
     if (empty) {
-        gn_grad_zero<<<dim3(static_cast<unsigned>(ceil_div(C, kLanes))), kLanes, 0, c.stream>>>(
-            static_cast<int>(C), dgamma, dbeta, atype);
+        gn_grad_samples<<<sgrid, kLanes, 0, c.stream>>>(nullptr, 0, static_cast<int>(C), dgamma,
+                                                        dbeta, atype);
         return finish_launch();
     }
     float *ws = static_cast<float *>(workspace);
@@ -871,6 +1097,22 @@ gn_status gn_silu_rows_backward(const void *dy, const void *x, const void *codes
     a.sums = f.sums;
     a.dgamma = dgamma;
     a.dbeta = dbeta;
+    if (p.strip.np > 0) {
+        a.tl.L = L;
+        a.tl.C = f.C;
+        StripArgs sa{};
+        sa.r = a;
+        sa.sums = grads && N > 1 ? ws : nullptr;
+        sa.P = p.strip.P;
+        sa.shift = p.strip.shift;
+        sa.strips = p.strip.strips;
+        sa.inv_m = f.inv_m;
+        launch_strip(sa, static_cast<unsigned>(N * p.strip.strips), p.strip.np, apply_silu != 0,
+                     codes != nullptr, dtype, c.stream);
+        if (sa.sums != nullptr)
+            gn_grad_samples<<<sgrid, kLanes, 0, c.stream>>>(ws, N, f.C, dgamma, dbeta, atype);
+        return finish_launch();
+    }
     with_pieces(C, dtype, [&](auto d, auto wc, auto tail) {
         using D = decltype(d);
         constexpr int W = decltype(wc)::value;

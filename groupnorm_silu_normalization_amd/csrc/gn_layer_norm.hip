@@ -640,7 +640,8 @@ int64_t backward_blocks(const LnShape &s, int64_t M) {
 }
 
 // Up to this many rows the columns' workgroups read x and dy again instead of
-// adding up partial rows.
+// adding up partial rows.  Measured on MI355X, bf16, partial rows / again:
+// (1024,1024) 22.4/17.5 us a call, (2048,1024) 22.3/24.5, (4096,256) 22.1/41.4.
 constexpr int64_t kFewRows = 1024;
 
 template <class D>

@@ -174,6 +174,8 @@ constexpr int kDppXor1 = 0xB1;        // quad_perm [1,0,3,2]
 constexpr int kDppXor2 = 0x4E;        // quad_perm [2,3,0,1]
 constexpr int kDppHalfMirror = 0x141; // lane i of a half row <-> 7 - i
 constexpr int kDppMirror = 0x140;     // lane i of a row <-> 15 - i
+constexpr int kDppRor4 = 0x124;       // rotations within a row of 16 lanes
+constexpr int kDppRor8 = 0x128;
 
 template <int N, class F>
 __device__ __forceinline__ uint32_t lane_fold(uint32_t v, F op) {

@@ -82,9 +82,12 @@ def test_backward(gn, shape, dtype, silu):
 
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("shape", [(1, 20011, 40, 8), (2, 9000, 64, 32), (1, 5000, 321, 3),
-                                   (1, 4096, 512, 32), (1, 2003, 2560, 32)])
+                                   (1, 4096, 512, 32), (1, 2003, 2560, 32), (2, 5000, 64, 64),
+                                   (1, 3001, 512, 1), (3, 1500, 2048, 4), (2, 4097, 8, 1),
+                                   (130, 40, 64, 16), (1, 4096, 128, 32), (3, 4095, 32, 16)])
 def test_many_rows(gn, shape, dtype):
-    """Chunks of several rounds of rows, with remainders."""
+    """Chunks of several rounds of rows, with remainders; samples on both sides
+    of the single launch's limits."""
     N, L, C, G = shape
     print("case gn backward rows %s %s" % (shape, dtype), flush=True)
     x, w, b, dy, mean, rstd = make(N, L, C, G, dtype, torch.float32, L)

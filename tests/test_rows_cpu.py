@@ -64,7 +64,7 @@ BIG = 1 << 61
     (layer_norm_backward, dict(x=None)), (layer_norm_backward, dict(codes=P[9], scales=P[10])),
     (layer_norm_backward, dict(x=None, codes=P[9])), (layer_norm_backward, dict(scales=P[9])),
     (layer_norm_backward, dict(dys=-1)), (layer_norm_backward, dict(xs=-1)),
-    (layer_norm_backward, dict(dxs=8)), (layer_norm_backward, dict(ws=None)),
+    (layer_norm_backward, dict(dxs=8)), (layer_norm_backward, dict(ws=None, M=5000)),
     (layer_norm_backward, dict(M=-4)), (layer_norm_backward, dict(C=-64)),
     (layer_norm_backward, dict(dtype=0x13)),
     (group_backward, dict(dy=None)), (group_backward, dict(dx=None)),
@@ -72,7 +72,7 @@ BIG = 1 << 61
     (group_backward, dict(x=None)), (group_backward, dict(codes=P[10], scales=P[11])),
     (group_backward, dict(G=0)), (group_backward, dict(G=7)), (group_backward, dict(G=-8)),
     (group_backward, dict(silu=2)), (group_backward, dict(N=-1)), (group_backward, dict(L=-1)),
-    (group_backward, dict(ws=None)), (group_backward, dict(N=1 << 40, L=1 << 30)),
+    (group_backward, dict(ws=None, L=50000)), (group_backward, dict(N=1 << 40, L=1 << 30)),
     (group_backward, dict(dtype=9)),
     (apply_save, dict(x=None)), (apply_save, dict(y=None)), (apply_save, dict(codes=None)),
     (apply_save, dict(scales=None)), (apply_save, dict(mean=None)), (apply_save, dict(rstd=None)),
@@ -126,24 +126,29 @@ def workspace(fn, *a):
 
 def test_workspace_sizes():
     ln, gb = gn.gn_layer_norm_rows_backward_workspace, gn.gn_silu_rows_backward_workspace
-    for M, C, dt in ((1, 1, 0), (5, 64, 1), (70000, 4096, 0), (3, 16384, 2), (1 << 40, 8, 0)):
+    for M, C, dt in ((5000, 1, 0), (2000, 64, 1), (70000, 4096, 0), (9000, 16384, 2),
+                     (1 << 40, 8, 0)):
         st, n = workspace(ln, M, C, dt)
         assert st == GnStatus.OK and 0 < n < 1 << 30 and n % (8 * C) == 0
         if M * C < 1 << 40:
             assert layer_norm_backward(M=M, C=C, xs=C, dys=C, dxs=C, dtype=dt,
                                        size=n - 1) == GnStatus.SCRATCH_TOO_SMALL
-    assert workspace(ln, 0, 64, 0) == (GnStatus.OK, 0)
+    for M in (0, 1, 1000):      # few rows need none
+        assert workspace(ln, M, 64, 0) == (GnStatus.OK, 0)
     assert workspace(ln, 4, 16385, 0)[0] == GnStatus.UNSUPPORTED
     assert workspace(ln, -1, 64, 0)[0] == GnStatus.INVALID_ARGUMENT
     assert ln(4, 64, 0, None) == GnStatus.INVALID_ARGUMENT
     for N, L, C, G, dt in ((1, 1, 1, 1, 0), (3, 7, 96, 8, 1), (1, 1 << 20, 256, 32, 0),
-                           (2, 5, 8192, 1, 2)):
+                           (2, 5, 8192, 1, 2), (2, 5, 64, 8, 0)):
         st, n = workspace(gb, N, L, C, G, dt)
         assert st == GnStatus.OK and 0 < n < 1 << 30
         assert group_backward(N=N, L=L, C=C, G=G, dtype=dt,
                               size=n - 1) == GnStatus.SCRATCH_TOO_SMALL
         assert group_backward(N=N, L=L, C=C, G=G, dtype=dt, size=-1) == GnStatus.SCRATCH_TOO_SMALL
+        assert group_backward(N=N, L=L, C=C, G=G, dtype=dt,
+                              ws=None) == GnStatus.INVALID_ARGUMENT
     assert workspace(gb, 1, 0, 64, 8, 0) == (GnStatus.OK, 0)
+    assert workspace(gb, 1, 100, 64, 8, 0) == (GnStatus.OK, 0)     # one launch, one sample
     assert workspace(gb, 1, 4, 64, 7, 0)[0] == GnStatus.INVALID_ARGUMENT
     assert workspace(gb, 1, 4, 8200, 8, 0)[0] == GnStatus.UNSUPPORTED
     assert gb(1, 4, 64, 8, 0, None) == GnStatus.INVALID_ARGUMENT
