@@ -17,8 +17,17 @@
 // reciprocal the hardware's, and dx two fmas on dt and x-mean.
 //
 // A lane keeps one piece of W consecutive channels for all its rows: a tile is
-// R rows of Pc pieces over the 256 lanes, and a row of more than 256 pieces is
-// cut into column blocks.  Channel parameters and sums stay in registers.
+// R rows of Pc pieces over the workgroup's lanes, and a longer row is cut into
+// column blocks.  Channel parameters and sums stay in registers.  The
+// workgroups advance through a sample together, a batch of tiles each, with the
+// next batch's loads in flight; small samples go in one launch instead
+// (gn_grad_strip).
+//
+// Measured on MI355X, bf16 (a 1 GiB copy reads and writes 5.1 TB/s there):
+// (1,1048576,256) pass 1 188 us (5.7 TB/s, VALU 71% busy), finish 5.8 us, pass
+// 2 280 us (5.75 TB/s); from the checkpoint, (1,65536,512), 29.0, 6.0 and 31.4
+// us (pass 1 bound by the VALU and its start and end, pass 2 by its stores);
+// apply that saves, (1,262144,512), 129 us (5.2 TB/s), restored 71.6 us (5.7).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -34,9 +43,14 @@ namespace gnsilu {
 namespace {
 
 constexpr int kLanes = 256;
-constexpr int kSumLanes = 512;  // pass 1 beyond kSmallBytes
-constexpr int kUnroll = 2;      // tiles per batch; two batches of loads are in flight ...
-constexpr int kInputUnroll = 4; // ... in pass 2 from x itself
+// Lanes of pass 1's workgroups beyond kSmallBytes: 256/512/1024 lanes took
+// 204/193/196 us at (1,1048576,256), and 7.0/8.3/11.9 at (1,4096,128).
+constexpr int kSumLanes = 512;
+// Tiles per batch; two batches of loads are in flight.  Pass 2 from x itself
+// takes more: 2/4/6 took 295/282/290 us at (1,1048576,256); from a checkpoint
+// 2/4 took 32.9/35.4 us at (1,65536,512).
+constexpr int kUnroll = 2;
+constexpr int kInputUnroll = 4;
 
 struct Tiles {
     int64_t L;        // rows per sample
@@ -466,7 +480,11 @@ __global__ __launch_bounds__(kLanes) void gn_grad_input(RowArgs a) {
 // takes a strip of whole groups of one sample (strip_c channels, P pieces of
 // a row, a power of two) and holds its x and dy in registers, NP pieces each
 // per lane, so both are read once.  Its channels' sums: the lanes of a wave
-// that hold the same piece by a butterfly, then the waves in order.
+// that hold the same piece by a butterfly, then the waves in order.  dx is
+// stored through the L2: strips narrower than a cache line write parts of
+// lines, which neighbouring strips on the same XCD complete there
+// ((1,4096,128): 22.0 us of kernel time with nontemporal stores and strips
+// dealt over the XCDs, 16.5 so).
 constexpr int kStripLanes = 1024;
 constexpr int kStripMaxPieces = 4;  // NP
 constexpr int kStripMaxRow = 32;    // P
@@ -475,6 +493,7 @@ struct StripArgs {
     float *sums;
     int P, shift;   // pieces of a strip's row, log2
     int strips;     // per sample
+    int xcd;        // the grid is a multiple of 8
     double inv_m;
 };
 
@@ -505,8 +524,11 @@ __global__ __launch_bounds__(kStripLanes) void gn_grad_strip(StripArgs sa) {
     __shared__ float red[2][kWaves][kStripMaxRow * W];
     __shared__ float coef[2][W];  // a and b of the strip's groups
     const int tid = threadIdx.x;
-    const int64_t n = blockIdx.x / static_cast<uint32_t>(sa.strips);
-    const int strip = static_cast<int>(blockIdx.x % static_cast<uint32_t>(sa.strips));
+    // Workgroups go to the 8 XCDs in turn; neighbouring strips, whose rows share
+    // cache lines, are given to workgroups of one XCD (one L2).
+    const uint32_t wg = sa.xcd ? (blockIdx.x % 8) * (gridDim.x / 8) + blockIdx.x / 8 : blockIdx.x;
+    const int64_t n = wg / static_cast<uint32_t>(sa.strips);
+    const int strip = static_cast<int>(wg % static_cast<uint32_t>(sa.strips));
     const int pc = tid & (sa.P - 1), r = tid >> sa.shift, R = kStripLanes >> sa.shift;
     const int c0 = strip * sa.P * W, c = c0 + pc * W, wide = sa.P * W;
     const int64_t row0 = n * a.tl.L;
@@ -620,7 +642,7 @@ __global__ __launch_bounds__(kStripLanes) void gn_grad_strip(StripArgs sa) {
         gradient(v[u], x, g);
 #pragma unroll
         for (int i = 0; i < W; ++i) o[i] = fmaf(g[i], ch.sc[i], fmaf(x[i], k1[i], k0[i]));
-        Piece<D, W>::template store<true>(dx + l * a.tl.C, o);
+        Piece<D, W>::template store<false>(dx + l * a.tl.C, o);
     }
 }
 
@@ -705,8 +727,9 @@ __global__ __launch_bounds__(kLanes) void gn_rows_restore(RowArgs a) {
 }
 
 // ---- host -----------------------------------------------------------------------
-constexpr int64_t kSumBlocks = 512;         // pass 1: workgroups of kSumLanes, 1 per CU
-constexpr int64_t kStreamBlocks = 2048;     // the other passes
+constexpr int64_t kSumBlocks = 512;         // pass 1: 2 per CU, each with its partial sums
+constexpr int64_t kStreamBlocks = 2048;     // the other passes (pass 2 at (1,1048576,256) with
+                                            // 1024/1280/2048/4096: 294/288/283/285 us)
 constexpr int64_t kSmallBytes = int64_t{16} << 20;  // x at most this: latency rules
 constexpr int64_t kMaxRun = 1024;           // rows a lane adds up in fp32
 
@@ -806,9 +829,10 @@ gn_status check_group_rows(int64_t N, int64_t L, int64_t C, int64_t G, int apply
 // kStripMaxBlocks workgroups, and x at most kStripMaxBytes, counted as the
 // 128-byte lines that a strip's rows lie in (a strip of one piece fetches eight
 // times what it uses).  Measured on MI355X, bf16, G = 32 (us a call, single
-// launch / three): (1,256,512) 18/26, (1,4096,128) 22.7/26, (2,4096,128)
-// 25.5/25.5, (8,4096,128) 39/27, (4,2048,512) 26.6/26.2, (8,2048,512) 42/33,
-// (8,1024,1024) 27/34, (8,128,8192) 25/53.
+// launch / three): (1,256,512) 18/25.5, (1,4096,128) 20.7/25.6, (2,4096,128)
+// 23.6/25.8, (4,2048,512) 23.8/26.3, (8,1024,1024) 26/34, (8,128,8192) 25/53;
+// beyond the limit, before stores were plain and strips mapped to XCDs,
+// (8,4096,128) 39/27, (8,2048,512) 42/33.
 constexpr int64_t kStripMaxBlocks = 256;
 constexpr int64_t kStripMaxBytes = int64_t{32} << 20;
 struct StripPlan {
@@ -1106,6 +1130,7 @@ gn_status gn_silu_rows_backward(const void *dy, const void *x, const void *codes
         sa.P = p.strip.P;
         sa.shift = p.strip.shift;
         sa.strips = p.strip.strips;
+        sa.xcd = N * p.strip.strips % 8 == 0;
         sa.inv_m = f.inv_m;
         launch_strip(sa, static_cast<unsigned>(N * p.strip.strips), p.strip.np, apply_silu != 0,
                      codes != nullptr, dtype, c.stream);

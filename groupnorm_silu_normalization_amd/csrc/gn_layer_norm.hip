@@ -21,6 +21,12 @@
 // workgroup's rows; the workgroup adds its row slots in a fixed order and
 // writes one partial row of C sums, and a second kernel adds the partial rows
 // (in fp64) in a fixed order: no atomics, the same bits on every call.
+//
+// Measured on MI355X, bf16 (a 1 GiB copy reads and writes 5.1 TB/s there):
+// (16384,4096) forward 45.9 us (5.85 TB/s), backward 78.6 us (5.1 TB/s) and
+// column sums 4.9 us; forward with the checkpoint (8192,2560) 23.6 us; backward
+// from the checkpoint (5001,1537) 16.6 us (five rows a slot: their latencies
+// and the sums' instructions bound it) and 3.9 us.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -551,7 +557,9 @@ constexpr int64_t kBackwardBlocks = 256;  // one per CU, or more when there are
 constexpr int64_t kMaxRun = 4096;         // more rows than a slot should add up in fp32
 
 // Lanes of a row: the fewest (a power of two) that hold it with `nv` pieces
-// each.
+// each.  Backward, one piece a lane leaves registers for twice the waves, two
+// halve a row's fixed work: one / two took 17.4 / 19.1 us of kernel time at
+// (5001,1537) from the checkpoint, 86.7 / 78 at (16384,4096).
 struct LnShape {
     int w, tpr, nv;
     bool tail;

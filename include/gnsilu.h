@@ -399,7 +399,8 @@ gn_status gn_layer_norm_rows(const void *x, int64_t x_stride, const void *gamma,
  *     dgamma[c] = sum over rows of dy*h, dbeta[c] = sum over rows of dy
  * The input comes as x or as its checkpoint (codes and scales), the other
  * null; with a checkpoint the formulas hold for the values it stands for.
- * The workspace is needed only when dgamma or dbeta is. */
+ * The workspace is needed only when dgamma or dbeta is, and for up to 1024
+ * rows not then (its size is 0). */
 gn_status gn_layer_norm_rows_backward_workspace(int64_t M, int64_t C, int dtype,
                                                 int64_t *bytes_out);
 gn_status gn_layer_norm_rows_backward(const void *dy, int64_t dy_stride, const void *x,
@@ -426,7 +427,8 @@ gn_status gn_apply_rows_save(const void *x, const float *mean, const float *rstd
  *     dgamma[c] = sum over n, l of dt*h, dbeta[c] = sum over n, l of dt
  *     a, b = means over the group (L*C/G values) of gamma*dt and gamma*dt*h
  *     dx = rstd*(gamma*dt - a - h*b)
- * The input comes as x or as its checkpoint, as for layer norm. */
+ * The input comes as x or as its checkpoint, as for layer norm.  The workspace
+ * of small single samples is empty (size 0). */
 gn_status gn_silu_rows_backward_workspace(int64_t N, int64_t L, int64_t C, int64_t G, int dtype,
                                           int64_t *bytes_out);
 gn_status gn_silu_rows_backward(const void *dy, const void *x, const void *codes,
