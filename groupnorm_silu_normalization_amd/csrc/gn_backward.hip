@@ -24,10 +24,10 @@
 // (gn_grad_strip).
 //
 // Measured on MI355X, bf16 (a 1 GiB copy reads and writes 5.1 TB/s there):
-// (1,1048576,256) pass 1 188 us (5.7 TB/s, VALU 71% busy), finish 5.8 us, pass
-// 2 280 us (5.75 TB/s); from the checkpoint, (1,65536,512), 29.0, 6.0 and 31.4
+// (1,1048576,256) pass 1 189 us (5.7 TB/s, VALU 79% busy), finish 5.8 us, pass
+// 2 279 us (5.8 TB/s); from the checkpoint, (1,65536,512), 28.7, 6.0 and 30.8
 // us (pass 1 bound by the VALU and its start and end, pass 2 by its stores);
-// apply that saves, (1,262144,512), 129 us (5.2 TB/s), restored 71.6 us (5.7).
+// apply that saves, (1,262144,512), 130 us (5.2 TB/s), restored 71 us (5.7).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

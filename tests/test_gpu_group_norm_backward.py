@@ -251,6 +251,89 @@ def test_gradient_against_differences(gn):
             assert abs(num - ana) <= (200 * ref.U + 1e-7) * scale
 
 
+@pytest.mark.parametrize("adt", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("shape", [(1, 40, 64, 8), (2, 3000, 40, 8), (1, 50, 321, 3)])
+def test_16bit_parameters_at_an_odd_element_offset(gn, shape, adt):
+    """Parameters at addresses 2 mod 4, in the single launch and in the passes:
+    dx as with fp32 copies of the same values, bit for bit, dw and db their
+    fp32 gradients rounded once."""
+    N, L, C, G = shape
+    x, w, b, dy, mean, rstd = cu(*make(N, L, C, G, torch.bfloat16, adt, C))
+    wb, bb = [torch.empty(C + 1, dtype=adt, device="cuda") for _ in range(2)]
+    wb[1:], bb[1:] = w, b
+    assert wb[1:].data_ptr() % 4 == 2
+    got = gn.group_norm_silu_rows_backward(dy, x, mean, rstd, wb[1:], bb[1:])
+    want = gn.group_norm_silu_rows_backward(dy, x, mean, rstd, w.float(), b.float())
+    assert torch.equal(got[0], want[0])
+    assert torch.equal(got[1], want[1].to(adt)) and torch.equal(got[2], want[2].to(adt))
+    y1 = gn.apply_rows(x, mean, rstd, wb[1:], bb[1:], checkpoint=True)[0]
+    assert torch.equal(y1, gn.apply_rows(x, mean, rstd, w.float(), b.float(), checkpoint=True)[0])
+
+
+def test_offsets_beyond_32_bits(gn):
+    """More than 2^31 values and 2^32 bytes: x and dy are zero but for the last
+    rows, whose gradients are those of these rows alone, the group's means
+    taken over all of it."""
+    C, G, n = 8, 2, 24
+    L = (1 << 28) + 1000
+    x = torch.zeros(1, L, C, dtype=torch.bfloat16, device="cuda")
+    dy = torch.zeros_like(x)
+    gen = torch.Generator().manual_seed(4)
+    xe = torch.randn(n, C, generator=gen).to(torch.bfloat16)
+    de = torch.randn(n, C, generator=gen).to(torch.bfloat16)
+    x[0, L - n:], dy[0, L - n:] = xe.cuda(), de.cuda()
+    w, b = torch.rand(C, generator=gen) + 0.5, torch.randn(C, generator=gen)
+    mean, rstd = torch.tensor([[0.25, -0.5]]), torch.tensor([[2.0, 0.5]])
+    dx, dw, db = gn.group_norm_silu_rows_backward(dy, x, *cu(mean, rstd, w, b))
+    mu = mean.double().repeat_interleave(4, 1)
+    rs = rstd.double().repeat_interleave(4, 1)
+    h = (xe.double() - mu) * rs
+    t = h * w.double() + b.double()
+    s = torch.sigmoid(t)
+    dt = de.double() * s * (1 + t * (1 - s))
+    a = (w * dt).sum(0).reshape(G, 4).sum(1).repeat_interleave(4) / (L * 4)
+    bb = (w * dt * h).sum(0).reshape(G, 4).sum(1).repeat_interleave(4) / (L * 4)
+    want = rs * (w * dt - a - h * bb)
+    # a few dozen fp32 roundings of the terms, and bf16's
+    bound = 64 * ref.U * rs * (w * dt.abs() + 1) + ref.rounded(want, torch.bfloat16)
+    ref.check(dx[0, L - n:], want, bound, "dx at the end")
+    ref.check(dw, (dt * h).sum(0), 64 * ref.U * (dt * h).abs().sum(0) + 1e-7, "dw")
+    ref.check(db, dt.sum(0), 64 * ref.U * dt.abs().sum(0) + 1e-7, "db")
+    # elsewhere dy is zero: dx = -rstd*(a + h0*b), below 1e-6 here, the same in
+    # every row
+    assert torch.equal(dx[0, 5], dx[0, L // 2]) and float(dx[0, 7].abs().max()) < 1e-6
+    del dy, dx
+    ck = gn.checkpoint_rows(x)
+    back = gn.restore_rows(ck)
+    assert torch.equal(back[0, L - n:].cpu(), ref.checkpoint(xe)[2].to(torch.bfloat16))
+    assert int(torch.count_nonzero(back[0, :L - n])) == 0
+
+
+def test_calls_from_two_threads(gn):
+    """Two host threads on streams of their own, interleaved: the bits of the
+    calls made alone."""
+    import threading
+    sets = [cu(*make(2, 700 + 300 * i, 96, 8, torch.bfloat16, torch.float32, i)) for i in range(2)]
+    alone = [gn.group_norm_silu_rows_backward(s[3], s[0], s[4], s[5], s[1], s[2]) for s in sets]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(i):
+        x, w, b, dy, mean, rstd = sets[i]
+        with torch.no_grad(), torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(30):
+                r = gn.group_norm_silu_rows_backward(dy, x, mean, rstd, w, b)
+                if not all(torch.equal(p, q) for p, q in zip(r, alone[i])):
+                    bad.append(i)
+
+    ts = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in ts:
+        t.start()
+    for t in ts:
+        t.join()
+    assert not bad
+
+
 def test_no_rows(gn):
     w = torch.ones(32, device="cuda")
     for N, L in ((0, 5), (2, 0)):
