@@ -257,8 +257,8 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 def _stream_handle(t):
     torch = _torch()
     if _raw_stream is not None:
-        return ctypes.c_void_p(_raw_stream(t.device.index))
-    return ctypes.c_void_p(torch.cuda.current_stream(t.device).cuda_stream)
+        return _raw_stream(t.device.index)
+    return torch.cuda.current_stream(t.device).cuda_stream
 
 
 def _ptr(t):
@@ -440,10 +440,15 @@ def _scales_shape(shape):
     return tuple(shape[:-1]) + ((shape[-1] + CHECKPOINT_BLOCK - 1) // CHECKPOINT_BLOCK,)
 
 
-def _empty_checkpoint(shape, device, dtype):
+def _empty_checkpoint(x):
+    """An unwritten checkpoint of x (of a supported dtype), made without
+    __init__'s checks."""
     torch = _torch()
-    return Checkpoint8(torch.empty(tuple(shape), dtype=torch.int8, device=device),
-                       torch.empty(_scales_shape(shape), dtype=torch.uint8, device=device), dtype)
+    ck = Checkpoint8.__new__(Checkpoint8)
+    ck.codes = torch.empty(x.shape, dtype=torch.int8, device=x.device)
+    ck.scales = torch.empty(_scales_shape(x.shape), dtype=torch.uint8, device=x.device)
+    ck.dtype = x.dtype
+    return ck
 
 
 def _row_stride(x):
@@ -539,7 +544,7 @@ def checkpoint_rows(x):
     step = _row_stride(x)
     if step is None or x.shape[-1] == 0:
         return None
-    ck = _empty_checkpoint(x.shape, x.device, x.dtype)
+    ck = _empty_checkpoint(x)
     code = _run(lib.gn_checkpoint_rows, x, _addr(x), step, _addr(ck.codes), _addr(ck.scales),
                 _rows_of(x), x.shape[-1], dtype_code(x.dtype))
     return _result(code, ck) if x.numel() else ck
@@ -605,7 +610,7 @@ def layer_norm_rows(x, weight=None, bias=None, eps=1e-6, *, stats=False, checkpo
         mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
         rstd = torch.empty_like(mean)
     if checkpoint:
-        ck = _empty_checkpoint(x.shape, x.device, x.dtype)
+        ck = _empty_checkpoint(x)
     r = (out, mean, rstd, ck) if checkpoint else (out, mean, rstd) if stats else out
     if not x.numel():
         return r
@@ -711,7 +716,7 @@ def _apply_rows_save(x, mean, rstd, weight, bias, apply_silu, out):
         _check_out(out, x)
         if not out.is_contiguous():
             raise ValueError("out must be contiguous")
-    ck = _empty_checkpoint(x.shape, x.device, x.dtype)
+    ck = _empty_checkpoint(x)
     code = _run(
         lib.gn_apply_rows_save, x, _addr(x), _addr(mean), _addr(rstd), _addr(weight), _addr(bias),
         _addr(out), _addr(ck.codes), _addr(ck.scales), N, L, C, G, 1 if apply_silu else 0,

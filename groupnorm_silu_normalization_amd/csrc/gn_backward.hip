@@ -219,18 +219,18 @@ template <class D, int W, bool TAIL, bool SAVED> struct Pair {
 
 // Adds the tile's R row slots' values by a fixed tree, into slot 0.
 template <int W, int NT>
-__device__ __forceinline__ void slot_tree(float (&red)[W][NT], int r, const Tiles &tl,
+__device__ __forceinline__ void slot_tree(float (&red)[W][NT], int r, int R, int Pc,
                                           float (&s)[W]) {
-    if (tl.R == 1) return;
+    if (R == 1) return;
     int p2 = 1;
-    while (p2 < tl.R) p2 <<= 1;
+    while (p2 < R) p2 <<= 1;
     __syncthreads();  // red is free
 #pragma unroll
     for (int i = 0; i < W; ++i) red[i][threadIdx.x] = s[i];
     for (int h = p2 >> 1; h > 0; h >>= 1) {
         __syncthreads();
-        if (r < h && r + h < tl.R) {
-            const int o = static_cast<int>(threadIdx.x) + h * tl.Pc;
+        if (r < h && r + h < R) {
+            const int o = static_cast<int>(threadIdx.x) + h * Pc;
 #pragma unroll
             for (int i = 0; i < W; ++i) red[i][threadIdx.x] = s[i] += red[i][o];
         }
@@ -267,8 +267,8 @@ __global__ __launch_bounds__(NT) void gn_grad_sums(RowArgs a) {
             s2[i] = fmaf(d, x[i], s2[i]);
         }
     });
-    slot_tree<W, NT>(red, at.r, tl, s1);
-    slot_tree<W, NT>(red, at.r, tl, s2);
+    slot_tree<W, NT>(red, at.r, tl.R, tl.Pc, s1);
+    slot_tree<W, NT>(red, at.r, tl.R, tl.Pc, s2);
     if (at.active && at.r == 0) {
         float *p = a.part + (at.n * tl.K + at.k) * 2 * tl.C + at.c;
 #pragma unroll
@@ -477,21 +477,23 @@ __global__ __launch_bounds__(kLanes) void gn_grad_input(RowArgs a) {
 }
 
 // The whole backward pass in one launch, for samples small enough: a workgroup
-// takes a strip of whole groups of one sample (strip_c channels, P pieces of
-// a row, a power of two) and holds its x and dy in registers, NP pieces each
-// per lane, so both are read once.  Its channels' sums: the lanes of a wave
-// that hold the same piece by a butterfly, then the waves in order.  dx is
-// stored through the L2: strips narrower than a cache line write parts of
-// lines, which neighbouring strips on the same XCD complete there
+// takes a strip of whole groups of one sample (P pieces of a row: the least
+// common multiple of a group and a piece) and holds its x and dy in registers,
+// NP pieces each per lane, so both are read once.  Its channels' sums: for P a
+// power of two up to 32 (POW2) the lanes of a wave that hold the same piece by
+// a butterfly, then the waves in order; else the row slots by a tree in LDS.
+// dx is stored through the L2: strips narrower than a cache line write parts
+// of lines, which neighbouring strips on the same XCD complete there
 // ((1,4096,128): 22.0 us of kernel time with nontemporal stores and strips
 // dealt over the XCDs, 16.5 so).
 constexpr int kStripLanes = 1024;
-constexpr int kStripMaxPieces = 4;  // NP
-constexpr int kStripMaxRow = 32;    // P
+constexpr int kStripMaxPieces = 4;    // NP
+constexpr int kStripMaxRow = 128;     // P
+constexpr int kStripMaxPow2Row = 32;  // P of the butterfly
 struct StripArgs {
-    RowArgs r;      // tl.L and tl.C; sums: [N][2][C] to write, or null
-    float *sums;
-    int P, shift;   // pieces of a strip's row, log2
+    RowArgs r;      // tl.L and tl.C
+    float *sums;    // [N][2][C] to write, or null
+    int P, shift;   // pieces of a strip's row; log2 for POW2
     int strips;     // per sample
     int xcd;        // the grid is a multiple of 8
     double inv_m;
@@ -516,20 +518,25 @@ __device__ __forceinline__ float fold_from(float v, int P) {
     return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
-template <class D, int W, bool SILU, bool SAVED, int NP>
+template <class D, int W, bool SILU, bool SAVED, int NP, bool POW2>
 __global__ __launch_bounds__(kStripLanes) void gn_grad_strip(StripArgs sa) {
     using T = typename D::storage;
     constexpr int kWaves = kStripLanes / 64;
+    static_assert(2 * kWaves * kStripMaxPow2Row == kStripLanes, "the waves' sums fill red");
     const RowArgs &a = sa.r;
-    __shared__ float red[2][kWaves][kStripMaxRow * W];
-    __shared__ float coef[2][W];  // a and b of the strip's groups
+    __shared__ float red[W][kStripLanes];
+    __shared__ float total[2][kStripMaxRow * W];  // per channel: sums, then times gamma
+    __shared__ float coef[2][W];                  // a and b of the strip's groups
     const int tid = threadIdx.x;
     // Workgroups go to the 8 XCDs in turn; neighbouring strips, whose rows share
     // cache lines, are given to workgroups of one XCD (one L2).
     const uint32_t wg = sa.xcd ? (blockIdx.x % 8) * (gridDim.x / 8) + blockIdx.x / 8 : blockIdx.x;
     const int64_t n = wg / static_cast<uint32_t>(sa.strips);
     const int strip = static_cast<int>(wg % static_cast<uint32_t>(sa.strips));
-    const int pc = tid & (sa.P - 1), r = tid >> sa.shift, R = kStripLanes >> sa.shift;
+    const int r = POW2 ? tid >> sa.shift : tid / sa.P;
+    const int R = POW2 ? kStripLanes >> sa.shift : kStripLanes / sa.P;
+    const int pc = tid - r * sa.P;
+    const bool active = POW2 || r < R;
     const int c0 = strip * sa.P * W, c = c0 + pc * W, wide = sa.P * W;
     const int64_t row0 = n * a.tl.L;
     using V = Pair<D, W, false, SAVED>;
@@ -555,7 +562,7 @@ __global__ __launch_bounds__(kStripLanes) void gn_grad_strip(StripArgs sa) {
     };
 #pragma unroll
     for (int u = 0; u < NP; ++u) {
-        if (r + int64_t{u} * R >= a.tl.L) break;
+        if (!active || r + int64_t{u} * R >= a.tl.L) break;
         float x[W], g[W];
         gradient(v[u], x, g);
 #pragma unroll
@@ -564,26 +571,48 @@ __global__ __launch_bounds__(kStripLanes) void gn_grad_strip(StripArgs sa) {
             s2[i] = fmaf(g[i], x[i], s2[i]);
         }
     }
-#pragma unroll
-    for (int i = 0; i < W; ++i) {
-        s1[i] = fold_from(s1[i], sa.P);
-        s2[i] = fold_from(s2[i], sa.P);
-    }
-    if ((tid & 63) < sa.P) {
+    float t1 = 0.0f, t2 = 0.0f;  // thread tid's channel, tid < wide
+    if constexpr (POW2) {
+        float *const flat = &red[0][0];  // [2][kWaves][P * W]
 #pragma unroll
         for (int i = 0; i < W; ++i) {
-            red[0][tid >> 6][pc * W + i] = s1[i];
-            red[1][tid >> 6][pc * W + i] = s2[i];
+            s1[i] = fold_from(s1[i], sa.P);
+            s2[i] = fold_from(s2[i], sa.P);
+        }
+        if ((tid & 63) < sa.P) {
+#pragma unroll
+            for (int i = 0; i < W; ++i) {
+                flat[(tid >> 6) * wide + pc * W + i] = s1[i];
+                flat[(kWaves + (tid >> 6)) * wide + pc * W + i] = s2[i];
+            }
+        }
+        __syncthreads();
+        if (tid < wide) {
+            t1 = flat[tid];
+            t2 = flat[kWaves * wide + tid];
+#pragma unroll
+            for (int w = 1; w < kWaves; ++w) {
+                t1 += flat[w * wide + tid];
+                t2 += flat[(kWaves + w) * wide + tid];
+            }
+        }
+    } else {
+        slot_tree<W, kStripLanes>(red, r, R, sa.P, s1);
+        slot_tree<W, kStripLanes>(red, r, R, sa.P, s2);
+        if (r == 0) {
+#pragma unroll
+            for (int i = 0; i < W; ++i) {
+                total[0][pc * W + i] = s1[i];
+                total[1][pc * W + i] = s2[i];
+            }
+        }
+        __syncthreads();
+        if (tid < wide) {
+            t1 = total[0][tid];
+            t2 = total[1][tid];
         }
     }
-    __syncthreads();
-    if (tid < wide) {  // one channel each
-        float t1 = red[0][0][tid], t2 = red[1][0][tid];
-#pragma unroll
-        for (int w = 1; w < kWaves; ++w) {
-            t1 += red[0][w][tid];
-            t2 += red[1][w][tid];
-        }
+    if (tid < wide) {
         const int cc = c0 + tid;
         t2 *= a.rstd[n * a.G + cc / a.Cg];
         if (sa.sums != nullptr) {
@@ -595,41 +624,35 @@ __global__ __launch_bounds__(kStripLanes) void gn_grad_strip(StripArgs sa) {
         }
         float ga[1];
         load_affine<1>(a.af.gamma, a.af.type, cc, 1.0f, ga);
-        red[0][0][tid] = t1 * ga[0];
-        red[1][0][tid] = t2 * ga[0];
+        total[0][tid] = t1 * ga[0];
+        total[1][tid] = t2 * ga[0];
     }
     __syncthreads();
-    // the groups' sums, in fp64: one group of `wide` channels, or several of a
-    // single piece
+    // the groups' sums in fp64, a wave each
     const int groups = wide / a.Cg;
-    if (tid < 64) {
+    const int wave = tid >> 6, lane = tid & 63;
+    if (wave < groups) {
         double ta = 0.0, tb = 0.0;
-        if (groups == 1) {
-            for (int e = tid; e < wide; e += 64) {
-                ta += static_cast<double>(red[0][0][e]);
-                tb += static_cast<double>(red[1][0][e]);
-            }
-#pragma unroll
-            for (int o = 1; o < 64; o <<= 1) {
-                ta += __shfl_xor(ta, o, 64);
-                tb += __shfl_xor(tb, o, 64);
-            }
-        } else if (tid < groups) {
-            for (int e = tid * a.Cg; e < (tid + 1) * a.Cg; ++e) {
-                ta += static_cast<double>(red[0][0][e]);
-                tb += static_cast<double>(red[1][0][e]);
-            }
+        for (int e = lane; e < a.Cg; e += 64) {
+            ta += static_cast<double>(total[0][wave * a.Cg + e]);
+            tb += static_cast<double>(total[1][wave * a.Cg + e]);
         }
-        if (tid < groups) {
-            coef[0][tid] = static_cast<float>(ta * sa.inv_m);
-            coef[1][tid] = static_cast<float>(tb * sa.inv_m);
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            ta += __shfl_xor(ta, o, 64);
+            tb += __shfl_xor(tb, o, 64);
+        }
+        if (lane == 0) {
+            coef[0][wave] = static_cast<float>(ta * sa.inv_m);
+            coef[1][wave] = static_cast<float>(tb * sa.inv_m);
         }
     }
     __syncthreads();
+    if (!active) return;
     float k0[W], k1[W];
 #pragma unroll
     for (int i = 0; i < W; ++i) {
-        const int g = groups == 1 ? 0 : i / a.Cg;
+        const int g = (pc * W + i) / a.Cg;
         k0[i] = -ch.rs[i] * coef[0][g];
         k1[i] = -ch.rs[i] * ch.rs[i] * coef[1][g];
     }
@@ -824,8 +847,8 @@ gn_status check_group_rows(int64_t N, int64_t L, int64_t C, int64_t G, int apply
     return GN_OK;
 }
 
-// The single launch: rows of whole pieces, groups of a power of two channels,
-// a strip's rows within kStripMaxPieces pieces per lane, at most
+// The single launch: rows of whole pieces, a strip's row of at most
+// kStripMaxRow pieces and its rows within kStripMaxPieces per lane, at most
 // kStripMaxBlocks workgroups, and x at most kStripMaxBytes, counted as the
 // 128-byte lines that a strip's rows lie in (a strip of one piece fetches eight
 // times what it uses).  Measured on MI355X, bf16, G = 32 (us a call, single
@@ -837,18 +860,22 @@ constexpr int64_t kStripMaxBlocks = 256;
 constexpr int64_t kStripMaxBytes = int64_t{32} << 20;
 struct StripPlan {
     int P = 0, shift = 0, np = 0, strips = 0;  // np = 0: not taken
+    bool pow2 = false;
 };
 StripPlan strip_plan(int64_t N, int64_t L, int64_t C, int64_t G, int w) {
     StripPlan s;
     const int64_t cg = C / G;
-    if (w == 1 || C % w != 0 || (cg & (cg - 1)) != 0) return s;
-    const int64_t wide = std::max<int64_t>(cg, w);
-    if (wide / w > kStripMaxRow || N * (C / wide) > kStripMaxBlocks) return s;
-    s.P = static_cast<int>(wide / w);
-    while ((1 << s.shift) < s.P) ++s.shift;
-    const int64_t np = ceil_div(L, kStripLanes / s.P);
+    if (w == 1 || C % w != 0) return s;
+    int64_t wide = cg;  // least common multiple with w, a power of two
+    while (wide % w != 0) wide *= 2;
+    const int64_t P = wide / w;
+    if (P > kStripMaxRow || N * (C / wide) > kStripMaxBlocks) return s;
+    const int64_t np = ceil_div(L, kStripLanes / P);
     if (np > kStripMaxPieces) return s;
-    if (N * L * C * (16 / w) * std::max(1, 8 / s.P) > kStripMaxBytes) return s;
+    if (N * L * C * (16 / w) * std::max<int64_t>(1, 8 / P) > kStripMaxBytes) return s;
+    s.P = static_cast<int>(P);
+    s.pow2 = P <= kStripMaxPow2Row && (P & (P - 1)) == 0;
+    while (s.pow2 && (1 << s.shift) < s.P) ++s.shift;
     s.np = np <= 1 ? 1 : (np <= 2 ? 2 : 4);
     s.strips = static_cast<int>(C / wide);
     return s;
@@ -888,24 +915,31 @@ bool backward_fits(int64_t N, const BackwardPlan &p) {
            N * p.sums.C < (int64_t{1} << 40);
 }
 
-void launch_strip(const StripArgs &sa, unsigned grid, int np, bool silu, bool saved, int dtype,
-                  hipStream_t st) {
-    auto by_np = [&](auto d, auto siluc, auto savedc) {
+void launch_strip(const StripArgs &sa, unsigned grid, const StripPlan &p, bool silu, bool saved,
+                  int dtype, hipStream_t st) {
+    auto by_np = [&](auto d, auto siluc, auto savedc, auto pow2c) {
         using D = decltype(d);
         constexpr int W = static_cast<int>(16 / sizeof(typename D::storage));
         constexpr bool SILU = decltype(siluc)::value != 0, SAVED = decltype(savedc)::value != 0;
-        if (np == 1)
-            gn_grad_strip<D, W, SILU, SAVED, 1><<<grid, kStripLanes, 0, st>>>(sa);
-        else if (np == 2)
-            gn_grad_strip<D, W, SILU, SAVED, 2><<<grid, kStripLanes, 0, st>>>(sa);
+        constexpr bool POW2 = decltype(pow2c)::value != 0;
+        if (p.np == 1)
+            gn_grad_strip<D, W, SILU, SAVED, 1, POW2><<<grid, kStripLanes, 0, st>>>(sa);
+        else if (p.np == 2)
+            gn_grad_strip<D, W, SILU, SAVED, 2, POW2><<<grid, kStripLanes, 0, st>>>(sa);
         else
-            gn_grad_strip<D, W, SILU, SAVED, 4><<<grid, kStripLanes, 0, st>>>(sa);
+            gn_grad_strip<D, W, SILU, SAVED, 4, POW2><<<grid, kStripLanes, 0, st>>>(sa);
+    };
+    auto by_row = [&](auto d, auto siluc, auto savedc) {
+        if (p.pow2)
+            by_np(d, siluc, savedc, IC<1>{});
+        else
+            by_np(d, siluc, savedc, IC<0>{});
     };
     auto by_flags = [&](auto d) {
         if (silu)
-            saved ? by_np(d, IC<1>{}, IC<1>{}) : by_np(d, IC<1>{}, IC<0>{});
+            saved ? by_row(d, IC<1>{}, IC<1>{}) : by_row(d, IC<1>{}, IC<0>{});
         else
-            saved ? by_np(d, IC<0>{}, IC<1>{}) : by_np(d, IC<0>{}, IC<0>{});
+            saved ? by_row(d, IC<0>{}, IC<1>{}) : by_row(d, IC<0>{}, IC<0>{});
     };
     switch (x_dtype(dtype)) {
         case GN_DTYPE_F16: by_flags(Fp16{}); break;
@@ -1132,7 +1166,7 @@ gn_status gn_silu_rows_backward(const void *dy, const void *x, const void *codes
         sa.strips = p.strip.strips;
         sa.xcd = N * p.strip.strips % 8 == 0;
         sa.inv_m = f.inv_m;
-        launch_strip(sa, static_cast<unsigned>(N * p.strip.strips), p.strip.np, apply_silu != 0,
+        launch_strip(sa, static_cast<unsigned>(N * p.strip.strips), p.strip, apply_silu != 0,
                      codes != nullptr, dtype, c.stream);
         if (sa.sums != nullptr)
             gn_grad_samples<<<sgrid, kLanes, 0, c.stream>>>(ws, N, f.C, dgamma, dbeta, atype);
