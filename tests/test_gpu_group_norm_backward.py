@@ -155,7 +155,8 @@ def test_absent_parameters(gn, which):
 def test_unaligned_rows_in_place_and_surroundings(gn, dtype):
     """x, dy and dx at odd element offsets of larger buffers; dx in dy's place
     and in x's; what lies before and behind stays as it was."""
-    for N, L, C, G in ((2, 37, 96, 8), (1, 50, 321, 3), (2, 9, 1001, 7)):
+    for N, L, C, G in ((2, 37, 96, 8), (1, 50, 321, 3), (2, 9, 1001, 7), (1, 9000, 96, 8),
+                       (2, 700, 4100, 4)):
         x, w, b, dy, mean, rstd = make(N, L, C, G, dtype, torch.float32, C)
         wg, bg, mg, rg = cu(w, b, mean, rstd)
         want = gn.group_norm_silu_rows_backward(dy.cuda(), x.cuda(), mg, rg, wg, bg)
@@ -191,8 +192,11 @@ def test_extremes(gn, dtype):
     assert int(torch.isnan(dw).sum()) == 1 and int(torch.isnan(db).sum()) == 1
 
 
-def test_same_bits_on_every_call_stream_and_replay(gn):
-    x, w, b, dy, mean, rstd = make(2, 3000, 320, 32, torch.bfloat16, torch.float32, 1)
+@pytest.mark.parametrize("shape", [(2, 3000, 320, 32), (2, 256, 320, 32), (3, 1000, 64, 16),
+                                   (1, 700, 128, 32)])
+def test_same_bits_on_every_call_stream_and_replay(gn, shape):
+    """In the passes and in the single launch, of several samples and one."""
+    x, w, b, dy, mean, rstd = make(*shape, torch.bfloat16, torch.float32, 1)
     x, w, b, dy, mean, rstd = cu(x, w, b, dy, mean, rstd)
 
     def call():

@@ -222,6 +222,27 @@ def test_in_place(gn, C, dtype):
     assert torch.equal(x2, y)
 
 
+@pytest.mark.parametrize("M", [301, 1500])
+@pytest.mark.parametrize("C", [24, 321, 1001, 2560])
+def test_in_place_with_checkpoints(gn, M, C):
+    """y in x's place while x is saved; dx in dy's place while x comes saved;
+    few rows and many."""
+    x, w, b, dy = cu(*make(M, C, torch.bfloat16, torch.float32, 5 * C))
+    y, mean, rstd, ck = gn.layer_norm_rows(x, w, b, EPS, checkpoint=True)
+    want = gn.layer_norm_rows_backward(dy, ck, mean, rstd, w)
+    x2, d2 = x.clone(), dy.clone()
+    r = gn.layer_norm_rows(x2, w, b, EPS, checkpoint=True, out=x2)
+    assert torch.equal(x2, y) and torch.equal(r[1], mean) and torch.equal(r[2], rstd)
+    assert torch.equal(r[3].codes, ck.codes) and torch.equal(r[3].scales, ck.scales)
+    got = gn.layer_norm_rows_backward(d2, ck, mean, rstd, w, out=d2)
+    for p, q in zip(got, want):
+        assert torch.equal(p, q)
+    # the saved rows in another type than the gradient's: only the codes count
+    ck32 = gn.Checkpoint8(ck.codes, ck.scales, torch.float32)
+    for p, q in zip(gn.layer_norm_rows_backward(dy, ck32, mean, rstd, w), want):
+        assert torch.equal(p, q)
+
+
 def test_same_bits_on_every_call_and_stream(gn):
     x, w, b, dy = cu(*make(3001, 1030, torch.bfloat16, torch.float32, 2))
     y, mean, rstd = gn.layer_norm_rows(x, w, b, EPS, stats=True)
