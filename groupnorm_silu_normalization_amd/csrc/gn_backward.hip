@@ -672,7 +672,10 @@ __global__ __launch_bounds__(kStripLanes) void gn_grad_strip(StripArgs sa) {
 // The apply step that also saves x (kApply, kApplySilu), or x saved alone
 // (kSave).  A block of the format lies in consecutive lanes of one row: the
 // plan makes Pc a multiple of the lanes that hold a block, or for shorter rows
-// a power of two.
+// a power of two.  What is stored is read much later, if at all, so it goes
+// past the caches -- but through the L2 where rows start off 16-byte
+// boundaries (TAIL), which joins their partial lines there: (2,16760,1001) bf16
+// with its restore took 65 us nontemporally, 57 so.
 enum { kApply = 0, kApplySilu = 1, kSave = 2 };
 template <class D, int W, bool TAIL, int MODE>
 __global__ __launch_bounds__(kLanes) void gn_rows_save(RowArgs a) {
@@ -717,11 +720,11 @@ __global__ __launch_bounds__(kLanes) void gn_rows_save(RowArgs a) {
             }
             T *p = y0 + d * a.y_stride;
             if (!TAIL || at.lo == 0)  // y may be x: only the lane's own channels
-                Piece<D, W>::template store<true>(p, o);
+                Piece<D, W>::template store<!TAIL>(p, o);
             else
                 store_from<D, W>(p, o, at.lo);
         }
-        store_block8<W, TAIL, true>(block8_encode<W>(x, E), E, codes0 + d * tl.C,
+        store_block8<W, TAIL, !TAIL>(block8_encode<W>(x, E), E, codes0 + d * tl.C,
                                     scales0 + d * nsb, at.c, at.lo);
     });
 }
@@ -745,7 +748,7 @@ __global__ __launch_bounds__(kLanes) void gn_rows_restore(RowArgs a) {
         if (!live || !at.active) return;
         float o[W];
         v.widen(at.c, edge, o);
-        Piece<D, W>::template store<true>(y0 + d * a.y_stride, o);
+        Piece<D, W>::template store<!TAIL>(y0 + d * a.y_stride, o);
     });
 }
 

@@ -236,10 +236,14 @@ __global__ __launch_bounds__(THREADS) void gn_layer_norm(LnArgs a) {
                 E = block8_exponent<D, W, kGroup>(r.v[j], Magnitudes<D, W>(lo[j]));
             if (!live || lo[j] >= W) continue;
             // A last piece's foreign channels get the value that their owner
-            // writes, computed alike.
-            Piece<D, W>::template store<SAVE>(y + m * a.y_stride + c[j], o);
+            // writes, computed alike.  Nontemporal only beside a checkpoint of
+            // 16-byte rows, as measured: y alone (16384,4096) 49.5 us, 46.0
+            // plain; with a checkpoint (8192,2560) 22.9, 24.8 plain; rows off
+            // 16-byte boundaries, whose partial lines the L2 joins, with a
+            // checkpoint and its restore (33520,1001) 63, 58 plain.
+            Piece<D, W>::template store<SAVE && !TAIL>(y + m * a.y_stride + c[j], o);
             if constexpr (SAVE)
-                store_block8<W, TAIL, true>(block8_encode<W>(f, E), E, a.codes_out + m * a.C,
+                store_block8<W, TAIL, !TAIL>(block8_encode<W>(f, E), E, a.codes_out + m * a.C,
                                             a.scales_out + m * nsb, c[j], lo[j]);
         }
     });
@@ -435,7 +439,7 @@ __global__ __launch_bounds__(THREADS) void gn_layer_norm_backward(LnArgs a) {
                     db[j][i] += d;
                 }
             }
-            if (lo[j] < W) Piece<D, W>::template store<true>(dx + m * a.y_stride + c[j], o);
+            if (lo[j] < W) Piece<D, W>::template store<!TAIL>(dx + m * a.y_stride + c[j], o);
         }
     });
     if (FEW || a.part == nullptr) return;
