@@ -439,7 +439,10 @@ __global__ __launch_bounds__(THREADS) void gn_layer_norm_backward(LnArgs a) {
                     db[j][i] += d;
                 }
             }
-            if (lo[j] < W) Piece<D, W>::template store<!TAIL>(dx + m * a.y_stride + c[j], o);
+            // Rows off 16-byte boundaries: (33520,1001) 56.0 us nontemporal, 54.5
+            // plain; from the checkpoint (5001,1537) 16.1 of kernel time, 17.2 plain.
+            if (lo[j] < W)
+                Piece<D, W>::template store<!TAIL || SAVED>(dx + m * a.y_stride + c[j], o);
         }
     });
     if (FEW || a.part == nullptr) return;
