@@ -12,9 +12,9 @@
 // one pass over x and dy that keeps two sums per channel gives everything
 // (pass 1); a small kernel finishes the sums; a second pass over x and dy
 // writes dx (pass 2).  Both passes are bound by memory and by the vector ALU
-// (about twenty instruction slots per element, SiLU's exponential and
-// reciprocal counting four each), so t is one fma, its exponential and
-// reciprocal the hardware's, and dx two fmas on dt and x-mean.
+// (about sixteen instructions per value, SiLU's exponential and reciprocal
+// among them), so t is one fma, its exponential and reciprocal the hardware's,
+// and dx two fmas on dt and x-mean.
 //
 // A lane keeps one piece of W consecutive channels for all its rows: a tile is
 // R rows of Pc pieces over the workgroup's lanes, and a longer row is cut into
@@ -802,7 +802,7 @@ int piece_width(int64_t C, int dtype) {
     const int w = static_cast<int>(16 / elem_bytes(dtype));
     return C < w ? 1 : w;
 }
-int block_lanes(int w) { return w == 1 ? 8 : kBlock8 / w; }  // powers of two
+int block_lanes(int w) { return w == 1 ? 8 : kBlock8 / w; }
 
 template <int V> using IC = std::integral_constant<int, V>;
 
