@@ -14,7 +14,7 @@
 // writes dx (pass 2).  Both passes are bound by memory and by the vector ALU
 // (about sixteen instructions per value, SiLU's exponential and reciprocal
 // among them), so t is one fma, its exponential and reciprocal the hardware's,
-// and dx two fmas on dt and x-mean.
+// and dx two fmas and a product on dt and x-mean.
 //
 // A lane keeps one piece of W consecutive channels for all its rows: a tile is
 // R rows of Pc pieces over the workgroup's lanes, and a longer row is cut into
@@ -179,6 +179,14 @@ template <int W> struct Channels {
 __device__ __forceinline__ float silu_grad(float t, float dy) {
     const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(t * -1.4426950408889634f));
     return dy * fmaf(t * s, 1.0f - s, s);
+}
+
+// dx = dt*scale + rstd*((x-mean)*k1 + k0), k1 = -rstd*b, k0 = -a.  The outer
+// rstd stays a product of its own: rstd*k1 leaves fp32's range (rstd above
+// 1e19, below 1e-19) where dx does not.
+__device__ __forceinline__ float input_grad(float dt, float x, float sc, float rs, float k1,
+                                            float k0) {
+    return fmaf(dt, sc, rs * fmaf(x, k1, k0));
 }
 
 // One row's piece of x (or its saved codes) and dy.
@@ -426,10 +434,9 @@ __global__ __launch_bounds__(kLanes) void gn_grad_samples(const float *sums, int
     add_samples(sums, N, C, static_cast<int>(blockIdx.x), dgamma, dbeta, type);
 }
 
-// Pass 2: dx = dt*scale - (x-mean)*rstd^2*b - rstd*a, from the rows that pass 1
-// read last to those that it read first, so that what the Infinity Cache still
-// holds of x and dy is read before it is replaced; dx is stored nontemporally
-// for the same reason.
+// Pass 2: dx from the rows that pass 1 read last to those that it read first,
+// so that what the Infinity Cache still holds of x and dy is read before it is
+// replaced; dx is stored nontemporally for the same reason.
 template <class D, int W, bool TAIL, bool SILU, bool SAVED>
 __global__ __launch_bounds__(kLanes) void gn_grad_input(RowArgs a) {
     using T = typename D::storage;
@@ -453,8 +460,8 @@ __global__ __launch_bounds__(kLanes) void gn_grad_input(RowArgs a) {
 #pragma unroll
     for (int i = 0; i < W; ++i) {
         const float *co = a.coef + 2 * (at.n * a.G + (at.c + i) / a.Cg);
-        k0[i] = -ch.rs[i] * co[0];
-        k1[i] = -ch.rs[i] * ch.rs[i] * co[1];
+        k0[i] = -co[0];
+        k1[i] = -ch.rs[i] * co[1];
     }
     T *dx = static_cast<T *>(a.y) + row0 * tl.C + at.c;
     st.run(at.k, load, [&](const V &v, int64_t d, bool live) {
@@ -465,7 +472,7 @@ __global__ __launch_bounds__(kLanes) void gn_grad_input(RowArgs a) {
         for (int i = 0; i < W; ++i) {
             float g = v.vy.get(i);
             if constexpr (SILU) g = silu_grad(fmaf(x[i], ch.sc[i], ch.be[i]), g);
-            o[i] = fmaf(g, ch.sc[i], fmaf(x[i], k1[i], k0[i]));
+            o[i] = input_grad(g, x[i], ch.sc[i], ch.rs[i], k1[i], k0[i]);
         }
         T *p = dx + d * tl.C;
         // dx may be dy or x: a lane writes only channels that no other reads
@@ -653,8 +660,8 @@ __global__ __launch_bounds__(kStripLanes) void gn_grad_strip(StripArgs sa) {
 #pragma unroll
     for (int i = 0; i < W; ++i) {
         const int g = (pc * W + i) / a.Cg;
-        k0[i] = -ch.rs[i] * coef[0][g];
-        k1[i] = -ch.rs[i] * ch.rs[i] * coef[1][g];
+        k0[i] = -coef[0][g];
+        k1[i] = -ch.rs[i] * coef[1][g];
     }
     T *dx = static_cast<T *>(a.y) + row0 * a.tl.C + c;
 #pragma unroll
@@ -664,7 +671,8 @@ __global__ __launch_bounds__(kStripLanes) void gn_grad_strip(StripArgs sa) {
         float x[W], g[W], o[W];
         gradient(v[u], x, g);
 #pragma unroll
-        for (int i = 0; i < W; ++i) o[i] = fmaf(g[i], ch.sc[i], fmaf(x[i], k1[i], k0[i]));
+        for (int i = 0; i < W; ++i)
+            o[i] = input_grad(g[i], x[i], ch.sc[i], ch.rs[i], k1[i], k0[i]);
         Piece<D, W>::template store<false>(dx + l * a.tl.C, o);
     }
 }

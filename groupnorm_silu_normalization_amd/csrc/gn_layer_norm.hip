@@ -425,7 +425,8 @@ __global__ __launch_bounds__(THREADS) void gn_layer_norm_backward(LnArgs a) {
         // With two pieces or more the widened values are made again rather than
         // kept across the sums, for their registers.
         if constexpr (NV > 1) r.opaque();
-        const float s0 = s[0] * a.inv_c, s1 = r.rstd * r.rstd * (s[1] * a.inv_c);
+        // rstd by rstd, not their square, which leaves fp32's range where dx does not
+        const float s0 = s[0] * a.inv_c, s1 = r.rstd * (r.rstd * (s[1] * a.inv_c));
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             float x[W], o[W];
