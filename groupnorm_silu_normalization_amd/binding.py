@@ -717,6 +717,8 @@ def _apply_rows_save(x, mean, rstd, weight, bias, apply_silu, out):
         if not out.is_contiguous():
             raise ValueError("out must be contiguous")
     ck = _empty_checkpoint(x)
+    if not x.numel():   # an empty tensor has no address to pass
+        return out, ck
     code = _run(
         lib.gn_apply_rows_save, x, _addr(x), _addr(mean), _addr(rstd), _addr(weight), _addr(bias),
         _addr(out), _addr(ck.codes), _addr(ck.scales), N, L, C, G, 1 if apply_silu else 0,

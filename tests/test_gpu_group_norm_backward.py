@@ -347,6 +347,25 @@ def test_no_rows(gn):
         assert dx.shape == x.shape and bool((dw == 0).all()) and bool((db == 0).all())
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_apply_that_saves_no_rows(gn, dtype):
+    """An empty batch goes through the saving apply step, and its checkpoint
+    through the backward pass."""
+    w = torch.ones(40, device="cuda")
+    for N, L in ((0, 5), (2, 0), (0, 0)):
+        x = torch.empty((N, L, 40), dtype=dtype, device="cuda")
+        st = torch.zeros((N, 4), device="cuda")
+        for out in (None, x):
+            y, ck = gn.apply_rows(x, st, st, w, w, out=out, checkpoint=True)
+            assert y.shape == x.shape and y.dtype == dtype and (out is None or y is out)
+            assert ck.shape == x.shape and tuple(ck.scales.shape) == (N, L, 2)
+            assert ck.dtype == dtype and gn.restore_rows(ck).shape == x.shape
+        dx, dw, db = gn.group_norm_silu_rows_backward(x, ck, st, st, w, w)
+        assert dx.shape == x.shape and bool((dw == 0).all()) and bool((db == 0).all())
+        with pytest.raises(ValueError):     # the checks come first
+            gn.apply_rows(x, st[:, :3], st, w, w, checkpoint=True)
+
+
 class _GroupNormSilu(torch.autograd.Function):
     """How a training program uses the calls: statistics, the apply step that
     keeps x in 8 bits (or x itself), the backward pass."""
