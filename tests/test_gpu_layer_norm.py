@@ -358,3 +358,49 @@ def test_offsets_beyond_32_bits(gn):
     d2 = gn.layer_norm_rows_backward(dy.cuda(), x.cuda(), mean, rstd, w.cuda())
     for p, q in zip(d1, d2):
         assert torch.equal(p, q)
+
+
+def corrected_bounds(x, w, b, eps):
+    """ref.layer_norm's values for fp32 rows with the bounds of a mean that is
+    corrected by the mean difference from it.  D = ref.ROW_DEPTH + 4 roundings
+    stand for a sum of differences, their own rounding and the quotient."""
+    y, mean, rstd, _, _, _ = ref.layer_norm(x, w, b, eps, torch.float32)
+    U, D = ref.U, ref.ROW_DEPTH + 4
+    x = x.double()
+    mean, rstd = mean.unsqueeze(-1), rstd.unsqueeze(-1)
+    d = x - mean
+    var = (d * d).mean(-1, keepdim=True)
+    e1 = D * U * x.abs().mean(-1, keepdim=True)             # the first mean
+    a = d.abs() + e1                                        # differences from it, at most
+    es = D * U * a.mean(-1, keepdim=True)                   # the shift
+    ec = es + U * (a + d.abs() + es)                        # the centred values
+    dv = (D * U * (a * a).mean(-1, keepdim=True) + 2 * (e1 + es) * es + es * es
+          + 3 * U * (e1 + es) ** 2 + U * var)
+    assert bool((dv < var + eps).all())
+    er = 0.5 * dv * (var + eps - dv) ** -1.5 + 3 * U * rstd
+    ey = (w.abs().double() * (rstd * ec + (d.abs() + ec) * er + 2 * U * (d * rstd).abs())
+          + U * (y.abs() + b.abs().double()))
+    em = es + U * mean.abs()
+    return (y, mean.squeeze(-1), rstd.squeeze(-1), 1.01 * ey + ref.rounded(y, torch.float32),
+            1.01 * em.squeeze(-1), 1.01 * er.squeeze(-1))
+
+
+@pytest.mark.parametrize("save", [False, True])
+@pytest.mark.parametrize("C", [1, 3, 8, 129, 768, 777, 1001, 4095, 4100, 12288, 16383])
+def test_fp32_rows_whose_spread_is_lost_in_their_size(gn, C, save):
+    """Equal values, and a spread of a few steps of fp32, far from zero: the
+    mean has to be nearer than the roundings of a plain fp32 sum."""
+    print("case layer_norm far rows C=%d save=%s" % (C, save), flush=True)
+    gen = torch.Generator().manual_seed(C)
+    x = torch.empty(6, C)
+    x[0], x[1], x[2] = 10000.1, -1000.3, 100.7
+    x[3] = 10000.0 + 0.01 * torch.randn(C, generator=gen)
+    x[4] = -3000.0 + 0.001 * torch.randn(C, generator=gen)
+    x[5] = torch.randn(C, generator=gen)
+    w = 1 + 0.3 * torch.randn(C, generator=gen)
+    b = 0.3 * torch.randn(C, generator=gen)
+    r = gn.layer_norm_rows(*cu(x, w, b), EPS, stats=True, checkpoint=save)
+    want = corrected_bounds(x, w, b, EPS)
+    for got, v, bound, name in zip(r, want[:3], want[3:], ("y", "mean", "rstd")):
+        ref.check(got, v, bound, "C=%d %s" % (C, name))
+    assert torch.equal(r[0][:3].cpu(), b.expand(3, C))      # equal values: beta
