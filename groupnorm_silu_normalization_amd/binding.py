@@ -382,7 +382,8 @@ def group_norm_silu_rows(x, num_groups, weight=None, bias=None, eps=1e-6, apply_
 
 
 def group_stats_rows(x, num_groups, eps=1e-6):
-    """Per-(n, g) fp32 mean and rstd of contiguous (N, L, C) rows (steps one and two)."""
+    """Per-(n, g) fp32 mean and rstd of contiguous (N, L, C) rows (steps one and two);
+    None where ``plan_rows`` has no tile layout for the shape."""
     torch = _torch()
     N, L, C = x.shape
     mean = torch.empty((N, num_groups), dtype=torch.float32, device=x.device)
@@ -398,8 +399,9 @@ def apply_rows(x, mean, rstd, weight=None, bias=None, apply_silu=True, out=None,
     """Step three alone on contiguous (N, L, C) rows, given per-(n, g) mean/rstd.
 
     checkpoint: also return x's 8-bit checkpoint, written in the same pass
-    ((y, Checkpoint8) instead of y; any C up to MAX_CHANNELS), for
-    ``group_norm_silu_rows_backward``."""
+    ((y, Checkpoint8) instead of y; any C up to MAX_CHANNELS, also those for
+    which ``group_stats_rows`` returns None: mean and rstd are then the
+    caller's), for ``group_norm_silu_rows_backward``."""
     if checkpoint:
         return _apply_rows_save(x, mean, rstd, weight, bias, apply_silu, out)
     torch = _torch()
@@ -732,7 +734,8 @@ def group_norm_silu_rows_backward(dy, x, mean, rstd, weight=None, bias=None, app
     (dx, dweight, dbias).
 
     x: the forward pass's input, or its Checkpoint8 (``apply_rows`` with
-    ``checkpoint``); mean, rstd: (N, G) as ``group_stats_rows`` returned them;
+    ``checkpoint``); mean, rstd: (N, G) fp32 as ``group_stats_rows`` returned
+    them (the caller's own at the widths that it declines);
     weight, bias: as in the forward pass.  dweight and dbias have the
     parameters' type (fp32 without any), and are None unless ``weight_grad``.
     None when the library declines the input."""

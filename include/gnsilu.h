@@ -414,14 +414,16 @@ gn_status gn_layer_norm_rows_backward(const void *dy, int64_t dy_stride, const v
  * any C <= GN_MAX_CHANNELS.  y is gn_apply_rows_dtype's bit for bit in bf16
  * and fp32; in fp16, where the last product of a value that a kernel stores
  * alone is rounded once and that of one in a wide access twice, a value may
- * differ by one fp16 step. */
+ * differ by one fp16 step.  mean and rstd: as gn_stats_rows writes them, or,
+ * for a C outside its supported set, the caller's own. */
 gn_status gn_apply_rows_save(const void *x, const float *mean, const float *rstd,
                              const void *gamma, const void *beta, void *y, void *codes,
                              void *scales, int64_t N, int64_t L, int64_t C, int64_t G,
                              int apply_silu, int dtype, void *stream);
 
 /* The backward pass of GroupNorm(+SiLU) over dense (N, L, C) rows, any
- * C <= GN_MAX_CHANNELS, with mean and rstd [N][G] as gn_stats_rows wrote them:
+ * C <= GN_MAX_CHANNELS, with mean and rstd [N][G] as gn_stats_rows wrote them
+ * (or the caller's own, for a C outside its supported set):
  *     h = (x-mean)*rstd, t = gamma*h + beta, s = sigmoid(t)
  *     dt = apply_silu ? dy*s*(1 + t*(1-s)) : dy
  *     dgamma[c] = sum over n, l of dt*h, dbeta[c] = sum over n, l of dt
