@@ -256,8 +256,9 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 def _stream_handle(t):
     torch = _torch()
-    if _raw_stream is not None:
+    if _raw_stream is not None and t.device.type == "cuda":
         return _raw_stream(t.device.index)
+    # raises for a tensor that is on no GPU, naming its device
     return torch.cuda.current_stream(t.device).cuda_stream
 
 

@@ -194,3 +194,15 @@ def test_row_strides():
     assert rs(x[..., ::2]) is None and rs(x[0, 0].expand(5, 10)) == 0
     assert rs(x.transpose(0, 1)) is None and rs(torch.zeros(3, 1).expand(3, 1)) == 1
     assert rs(torch.zeros(7)[3:4]) == 1
+
+
+def test_calls_without_a_device_check_name_the_cause_on_cpu_tensors():
+    """Steps that take any tensor's address report what torch says of its
+    device (ValueError) or of the missing GPU, not of a stream."""
+    x, st = torch.zeros(1, 4, 64), torch.zeros(1, 8)
+    for call in (lambda: gn.group_stats_rows(x, 8), lambda: gn.apply_rows(x, st, st),
+                 lambda: gn.profile_rows(x, 8, None, None, 1e-6, True, x, 1)):
+        with pytest.raises((ValueError, RuntimeError, AssertionError)) as e:
+            with torch.no_grad():
+                call()
+        assert "Stream" not in str(e.value)
