@@ -860,15 +860,17 @@ gn_status check_group_rows(int64_t N, int64_t L, int64_t C, int64_t G, int apply
 
 // The single launch: rows of whole pieces, a strip's row of at most
 // kStripMaxRow pieces and its rows within kStripMaxPieces per lane, at most
-// kStripMaxBlocks workgroups, and x at most kStripMaxBytes, counted as the
-// 128-byte lines that a strip's rows lie in (a strip of one piece fetches eight
-// times what it uses).  Measured on MI355X, bf16, G = 32 (us a call, single
-// launch / three): (1,256,512) 18/25.5, (1,4096,128) 20.7/25.6, (2,4096,128)
-// 23.6/25.8, (4,2048,512) 23.8/26.3, (8,1024,1024) 26/34, (8,128,8192) 25/53;
-// beyond the limit, before stores were plain and strips mapped to XCDs,
-// (8,4096,128) 39/27, (8,2048,512) 42/33.
+// kStripMaxBlocks workgroups (so x at most 16 MiB).  A strip of one piece
+// fetches eight times what it uses of each line, so these take x of at most
+// kStripNarrowBytes.  Measured on MI355X, bf16, G = 32, us in a captured graph
+// (eager calls, where a launch costs 3 us of host time), single launch / three:
+// one piece (1,4096,128) 19.9/16.1 (19.9/24.5), (4,4096,128) 21.6/20.4
+// (22.3/24.4), beyond the limit (5,4096,128) 25.2/22.3 (24.6/24.0),
+// (8,4096,128) 24.7/24.3 (24.5/24.8); two (2,2048,512) 20.3/20.4 (20.6/24.1),
+// (8,2048,512) 26.3/33.1 (25.7/32.8); four (8,1024,1024) 25.7/33.4 (25.1/33.6);
+// more (1,256,512) 7.9/14.9 (16.3/23.8), (4,64,8192) 15/29.6.
 constexpr int64_t kStripMaxBlocks = 256;
-constexpr int64_t kStripMaxBytes = int64_t{32} << 20;
+constexpr int64_t kStripNarrowBytes = int64_t{4} << 20;
 struct StripPlan {
     int P = 0, shift = 0, np = 0, strips = 0;  // np = 0: not taken
     bool pow2 = false;
@@ -883,7 +885,7 @@ StripPlan strip_plan(int64_t N, int64_t L, int64_t C, int64_t G, int w) {
     if (P > kStripMaxRow || N * (C / wide) > kStripMaxBlocks) return s;
     const int64_t np = ceil_div(L, kStripLanes / P);
     if (np > kStripMaxPieces) return s;
-    if (N * L * C * (16 / w) * std::max<int64_t>(1, 8 / P) > kStripMaxBytes) return s;
+    if (P == 1 && N * L * C * (16 / w) > kStripNarrowBytes) return s;
     s.P = static_cast<int>(P);
     s.pow2 = P <= kStripMaxPow2Row && (P & (P - 1)) == 0;
     while (s.pow2 && (1 << s.shift) < s.P) ++s.shift;

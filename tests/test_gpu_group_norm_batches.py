@@ -2,7 +2,7 @@
 checkpoints where a workgroup takes several batches of rows (a round of the
 grid, 2048 workgroups of 256 lanes, holds 2 pieces a lane of 16 bytes, 4 in the
 second pass from x itself), the last one partial; the single launch at its
-widest strip; a block trained from saved inputs.  Against 64 bits."""
+widest and largest strips; a block trained from saved inputs.  Against 64 bits."""
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -109,8 +109,9 @@ def test_rows_saved_and_restored(gn, M, C, dtype):
 @pytest.mark.parametrize("shape,dtype", [
     ((1, 30, 2048, 2), BF16), ((3, 32, 1024, 1), FP16), ((2, 25, 1024, 2), FP32),   # 128 pieces
     ((2, 33, 1016, 1), BF16),                                                       # 127
-    ((1, 61, 1024, 2), BF16), ((1, 31, 2048, 4), FP16)])                            # 64
-def test_widest_strips_of_the_single_launch(gn, shape, dtype, silu, saved):
+    ((1, 61, 1024, 2), BF16), ((1, 31, 2048, 4), FP16),                             # 64
+    ((6, 2048, 512, 32), BF16), ((5, 2047, 384, 24), FP32)])                        # 2, 4
+def test_widest_and_largest_strips_of_the_single_launch(gn, shape, dtype, silu, saved):
     print("case gn strips %s %s silu=%s saved=%s" % (shape, dtype, silu, saved), flush=True)
     x, w, b, dy, mean, rstd = make(*shape, dtype, shape[1])
     given = gn.checkpoint_rows(x.cuda()) if saved else x.cuda()
