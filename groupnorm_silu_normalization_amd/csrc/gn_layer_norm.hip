@@ -267,7 +267,8 @@ __global__ __launch_bounds__(THREADS) void gn_layer_norm(LnArgs a) {
             // 16-byte rows, as measured: y alone (16384,4096) 49.5 us, 46.0
             // plain; with a checkpoint (8192,2560) 22.9, 24.8 plain; rows off
             // 16-byte boundaries, whose partial lines the L2 joins, with a
-            // checkpoint and its restore (33520,1001) 63, 58 plain.
+            // checkpoint and its restore (33520,1001) 61.5, 53.8 plain,
+            // (8001,4097) 79.6, 75.0 plain, (100001,257) 73, 66 plain.
             Piece<D, W>::template store<SAVE && !TAIL>(y + m * a.y_stride + c[j], o);
             if constexpr (SAVE)
                 store_block8<W, TAIL, !TAIL>(block8_encode<W>(f, E), E, a.codes_out + m * a.C,
@@ -467,8 +468,14 @@ __global__ __launch_bounds__(THREADS) void gn_layer_norm_backward(LnArgs a) {
                     db[j][i] += d;
                 }
             }
-            // Rows off 16-byte boundaries: (33520,1001) 56.0 us nontemporal, 54.5
-            // plain; from the checkpoint (5001,1537) 16.1 of kernel time, 17.2 plain.
+            // Rows off 16-byte boundaries: from the checkpoint nontemporal, from x
+            // itself plain.  Measured, us nontemporal / plain, with dx in new
+            // memory each call (and in the memory of the call before): saved
+            // (12000,1001) 23.5/24.8, (33520,1001) 53.3/55.1 (52.3/51.7),
+            // (40001,1537) 99/102.6 (97.8/100.2), fp32 (8001,1001) 19.5/22.3; x
+            // itself (12000,1001) 23.6/26.9 (24.0/23.9), (33520,1001) 55.7/57.2
+            // (55.0/53.5), (40001,1537) 103/106 (102/104), (100001,257) 64.3/63.5
+            // (64.4/62.0): plain gains where the caches still hold dx's lines.
             if (lo[j] < W)
                 Piece<D, W>::template store<!TAIL || SAVED>(dx + m * a.y_stride + c[j], o);
         }
@@ -585,8 +592,9 @@ __global__ __launch_bounds__(kColLanes *kColParts) void gn_column_sums(const flo
 }
 
 // ---- host -----------------------------------------------------------------------
-// Workgroups: eight waves' worth of lanes per SIMD of 256 CUs forward, four
-// backward, where each workgroup writes a partial row.
+// Workgroups: eight waves' worth of lanes per SIMD of 256 CUs forward; backward,
+// where each workgroup writes a partial row, four, or two where a workgroup has
+// 512 lanes (two pieces a lane or more, for their registers).
 constexpr int64_t kForwardLanes = int64_t{2048} * 256;
 constexpr int64_t kBackwardBlocks = 256;  // one per CU, or more when there are
 constexpr int64_t kMaxRun = 4096;         // more rows than a slot should add up in fp32

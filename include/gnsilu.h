@@ -366,9 +366,11 @@ gn_status gn_plan_rows_dtype(int64_t N, int64_t L, int64_t C, int64_t G, int dty
  * magnitude as an fp32 number; a value x is kept as the code
  *     q = clamp(round_half_even(x * 2^(133-E)), -127, 127)
  * and stands for q * 2^(E-133) (elements and scales of the OCP MX format
- * MXINT8).  The error is at most 2^(E-134), one part in 128 of the block's
- * largest magnitude, and 2^(E-133) for magnitudes in the topmost half step of
- * the block's range, which the clamp takes.  Scaling by powers of two is
+ * MXINT8).  The error is at most 2^(E-134), and 2^(E-133) for magnitudes in the
+ * topmost half step of the block's range, which the clamp takes.  For E >= 1
+ * the former is at most one part in 128 of the block's largest magnitude; in
+ * a block of E = 0 (magnitudes below 2^-126) it is 2^-134 however small the
+ * values are: what lies below that comes back as zero.  Scaling by powers of two is
  * exact, so the codes depend on x alone.  A block that holds an infinity or a
  * NaN has E = 255 and stands for NaN throughout.  codes: int8 [M][C], scales:
  * uint8 [M][ceil(C / GN_CHECKPOINT_BLOCK)], dense, any alignment: 1 + 1/32
@@ -386,6 +388,8 @@ gn_status gn_restore_rows(const void *codes, const void *scales, void *x, int64_
 /* Layer norm of M rows of C values, C <= GN_LAYER_NORM_MAX_CHANNELS:
  *     mean = sum(x)/C, var = sum((x-mean)^2)/C, rstd = 1/sqrt(var + eps)
  *     y = gamma*(x-mean)*rstd + beta
+ * The statistics are fp32: spreads above 1e17, or below 1e-18 with an eps
+ * below their square, lie outside its range.
  * mean_out / rstd_out: fp32 [M] or null.  codes / scales: the checkpoint of x,
  * both or neither, written in the same pass. */
 gn_status gn_layer_norm_rows(const void *x, int64_t x_stride, const void *gamma, const void *beta,
