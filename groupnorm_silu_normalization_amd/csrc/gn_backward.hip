@@ -416,15 +416,53 @@ __global__ __launch_bounds__(kLanes) void gn_grad_groups(FinishArgs a) {
     }
 }
 
-// dgamma and dbeta of N samples (zeros for none), 256 channels per workgroup.
+// dgamma and dbeta of N samples (zeros for none): a workgroup takes 16 channels
+// and 16 parts of the samples, each part's in order with eight samples' loads
+// in flight, then the parts in a fixed order, in fp64.  One lane a channel, a
+// sample at a time, took 0.27 us a sample: (10000,64,64) 2855 us, 490 so,
+// (2000,256,64) 605 and 132, (128,64,16) 38 and 25.
+constexpr int kSampleLanes = 16, kSampleParts = kLanes / kSampleLanes;
 __device__ __forceinline__ void add_samples(const float *sums, int64_t N, int C, int block,
                                             void *dgamma, void *dbeta, int type) {
-    const int c = block * kLanes + static_cast<int>(threadIdx.x);
-    if (c >= C) return;
+    constexpr int kWaves = kLanes / 64, kBatch = 8;
+    __shared__ double red[2][kWaves][kSampleLanes];
+    const int lane = threadIdx.x % kSampleLanes, part = threadIdx.x / kSampleLanes;
+    const int c = block * kSampleLanes + lane;
     double s1 = 0.0, s2 = 0.0;
-    for (int64_t n = 0; n < N; ++n) {
-        s1 += static_cast<double>(sums[n * 2 * C + c]);
-        s2 += static_cast<double>(sums[n * 2 * C + C + c]);
+    if (c < C) {
+        const float *p = sums + c;
+        const int64_t step = 2 * static_cast<int64_t>(C);
+        for (int64_t n = part; n < N; n += kBatch * kSampleParts) {
+            float v1[kBatch], v2[kBatch];
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                const int64_t m = n + u * kSampleParts < N ? n + u * kSampleParts : N - 1;
+                v1[u] = p[m * step];
+                v2[u] = p[m * step + C];
+            }
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                const bool in = n + u * kSampleParts < N;
+                s1 += in ? static_cast<double>(v1[u]) : 0.0;
+                s2 += in ? static_cast<double>(v2[u]) : 0.0;
+            }
+        }
+    }
+#pragma unroll
+    for (int o = kSampleLanes; o < 64; o <<= 1) {
+        s1 += __shfl_xor(s1, o, 64);
+        s2 += __shfl_xor(s2, o, 64);
+    }
+    if ((threadIdx.x & 63) < kSampleLanes) {
+        red[0][threadIdx.x >> 6][lane] = s1;
+        red[1][threadIdx.x >> 6][lane] = s2;
+    }
+    __syncthreads();
+    if (part > 0 || c >= C) return;
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) {
+        s1 += red[0][w][lane];
+        s2 += red[1][w][lane];
     }
     if (dbeta != nullptr) store_affine(dbeta, type, c, static_cast<float>(s1));
     if (dgamma != nullptr) store_affine(dgamma, type, c, static_cast<float>(s2));
@@ -1126,7 +1164,7 @@ gn_status gn_silu_rows_backward(const void *dy, const void *x, const void *codes
                      p.total > 0 ? workspace : nullptr},
                     &c);
     if (st != GN_OK) return st;
-    const dim3 sgrid(static_cast<unsigned>(ceil_div(C, kLanes)));
+    const unsigned sgrid = static_cast<unsigned>(ceil_div(C, kSampleLanes));
     const int atype = affine_type(dtype);
     if (empty) {
         gn_grad_samples<<<sgrid, kLanes, 0, c.stream>>>(nullptr, 0, static_cast<int>(C), dgamma,
@@ -1209,7 +1247,7 @@ gn_status gn_silu_rows_backward(const void *dy, const void *x, const void *codes
             a.tl = p.input;
             dim3 grid = grid_of(N, a.tl);
             a.rows_end = grid.x;
-            if (grads && N > 1) grid.x += static_cast<unsigned>(ceil_div(C, kLanes));
+            if (grads && N > 1) grid.x += sgrid;
             gn_grad_input<D, W, TAIL, SILU, SAVED><<<grid, kLanes, 0, c.stream>>>(a);
         };
         auto by_saved = [&](auto silu) {

@@ -105,6 +105,23 @@ def test_rows_saved_and_restored(gn, M, C, dtype):
 
 
 @pytest.mark.parametrize("saved", [False, True])
+@pytest.mark.parametrize("shape,dtype", [
+    ((2, 9, 24, 3), BF16), ((17, 3, 24, 3), FP32), ((128, 5, 64, 1), BF16), ((129, 5, 64, 1), FP16),
+    ((255, 2, 32, 1), FP32), ((257, 3, 40, 8), BF16), ((1025, 9, 33, 3), FP32),
+    ((3000, 16, 64, 8), BF16), ((1100, 3, 7, 7), FP16), ((600, 2, 200, 2), BF16)])
+def test_weight_gradients_of_many_samples(gn, shape, dtype, saved):
+    """Samples on both sides of a round of the sum over samples (128), in the
+    single launch (up to 256) and behind the passes."""
+    print("case gn samples %s %s saved=%s" % (shape, dtype, saved), flush=True)
+    N, L, C, G = shape
+    x, w, b, dy, mean, rstd = make(*shape, dtype, N)
+    given = gn.checkpoint_rows(x.cuda()) if saved else x.cuda()
+    if saved:
+        x = ref.checkpoint(x)[2]
+    check_backward(gn, dy, x, given, mean, rstd, w, b, True, (shape, dtype, saved))
+
+
+@pytest.mark.parametrize("saved", [False, True])
 @pytest.mark.parametrize("silu", [False, True])
 @pytest.mark.parametrize("shape,dtype", [
     ((1, 30, 2048, 2), BF16), ((3, 32, 1024, 1), FP16), ((2, 25, 1024, 2), FP32),   # 128 pieces
