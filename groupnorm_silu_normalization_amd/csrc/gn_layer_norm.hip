@@ -240,7 +240,8 @@ __global__ __launch_bounds__(THREADS) void gn_layer_norm(LnArgs a) {
         float shift = 0.0f, var = q[0] / fc;
         if constexpr (kCorrect) {
             shift = q[1] / fc;
-            var -= shift * shift;
+            // an fma: its product is not infinite where var is
+            var = fmaf(-shift, shift, var);
             var = var < 0.0f ? 0.0f : var;  // a NaN stays
         }
         const float rstd = 1.0f / sqrtf(var + a.eps);

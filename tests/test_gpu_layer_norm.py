@@ -404,3 +404,20 @@ def test_fp32_rows_whose_spread_is_lost_in_their_size(gn, C, save):
     for got, v, bound, name in zip(r, want[:3], want[3:], ("y", "mean", "rstd")):
         ref.check(got, v, bound, "C=%d %s" % (C, name))
     assert torch.equal(r[0][:3].cpu(), b.expand(3, C))      # equal values: beta
+
+
+@pytest.mark.parametrize("C", [5, 777, 1001, 4095, 12288])
+def test_fp32_rows_of_equal_values_whose_squares_are_infinite(gn, C):
+    """Equal values so large that the squares of a sum's roundings leave fp32:
+    the normalised values are still at most a few roundings from zero."""
+    b = torch.randn(C, generator=torch.Generator().manual_seed(C))
+    # the values above times a power of two: their sums are rounded alike
+    x = (torch.tensor([10000.1, -1000.3, 100.7]) * 2.0 ** 90).unsqueeze(1).expand(3, C)
+    for save in (False, True):
+        r = gn.layer_norm_rows(x.contiguous().cuda(), None, b.cuda(), EPS, stats=True,
+                               checkpoint=save)
+        y, mean = r[0].cpu(), r[1].cpu()
+        # 2^-12, the root of a rounding: y is the rounding of a difference over
+        # the root of the rounding of its square, or over infinity
+        assert float((y - b).abs().max()) <= 2.0 ** -12
+        assert bool(((mean - x[:, 0]).abs() <= 4 * ref.U * x[:, 0].abs()).all())
