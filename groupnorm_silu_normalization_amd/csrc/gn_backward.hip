@@ -44,7 +44,9 @@ namespace {
 
 constexpr int kLanes = 256;
 // Lanes of pass 1's workgroups beyond kSmallBytes: 256/512/1024 lanes took
-// 204/193/196 us at (1,1048576,256), and 7.0/8.3/11.9 at (1,4096,128).
+// 204/193/196 us at (1,1048576,256), and 7.0/8.3/11.9 at (1,4096,128).  Many
+// samples that one batch of 256 lanes holds stay with 256: 256/512 took 93/162
+// us at (10000,64,64), 799/1540 at (100000,16,32).
 constexpr int kSumLanes = 512;
 // Tiles per batch; two batches of loads are in flight.  Pass 2 from x itself
 // takes more: 2/4/6 took 295/282/290 us at (1,1048576,256); from a checkpoint
@@ -76,9 +78,9 @@ struct RowArgs {
     int G, Cg;
     Affine af;
     Tiles tl;
-    // pass 2 of several samples: workgroups from `rows_end` on add up dgamma
-    // and dbeta
-    uint32_t rows_end;
+    // pass 2 of several samples: the first workgroups, beside the others, add up
+    // dgamma and dbeta
+    uint32_t sample_blocks;
     int64_t N;
     const float *sums;  // [N][2][C]
     void *dgamma, *dbeta;
@@ -89,8 +91,7 @@ template <int W, bool TAIL> struct Place {
     int64_t n, k;
     int r, c, lo;
     bool active;
-    __device__ __forceinline__ explicit Place(const Tiles &t) {
-        const uint32_t b = blockIdx.x;
+    __device__ __forceinline__ explicit Place(const Tiles &t, uint32_t b = blockIdx.x) {
         const uint32_t nk = b / static_cast<uint32_t>(t.ncb);
         const int cb = static_cast<int>(b - nk * static_cast<uint32_t>(t.ncb));
         const uint32_t ns = nk / static_cast<uint32_t>(t.K);
@@ -295,24 +296,29 @@ __global__ __launch_bounds__(NT) void gn_grad_sums(RowArgs a) {
 // sum dt*h.  A tile of whole groups (Cg <= 64) also gives their a and b; one
 // sample alone its dgamma and dbeta.  The narrowest tile that holds a group
 // (16 to 64 channels) has the most parts and so the shortest chain of loads.
-constexpr int kFinishThreads = 1024;
+// FEW: no more partials than a part has loads in flight, as in many small
+// samples: each of four waves takes a tile of up to 64 channels.  1024 threads a
+// tile took (200,3,8192) 559 us, (10000,64,64) 486 and (500,256,320) 176.
+constexpr int kFinishThreads = 1024, kFinishBatch = 8, kFewThreads = 256;
 struct FinishArgs {
     const float *part;
     const float *rstd;
     float *sums, *coef;
     void *dgamma, *dbeta;  // null unless N = 1 and wanted
-    int64_t K;
+    int64_t K, all_tiles;  // all_tiles: of the samples together
     int C, G, Cg, tile_c, tiles, width;
     double inv_m;
     Affine af;
 };
-__global__ __launch_bounds__(kFinishThreads) void gn_grad_finish(FinishArgs a) {
-    __shared__ double red[2][kFinishThreads / 64 * 64];
-    const int tid = threadIdx.x;
-    const int wide = 1 << a.width, parts = kFinishThreads >> a.width;
-    const int lane = tid & (wide - 1), r = tid >> a.width;
-    const int64_t n = blockIdx.x / a.tiles;
-    const int c = static_cast<int>(blockIdx.x % a.tiles) * a.tile_c + lane;
+template <bool FEW>
+__global__ __launch_bounds__(FEW ? kFewThreads : kFinishThreads) void gn_grad_finish(FinishArgs a) {
+    const int tid = FEW ? threadIdx.x & 63 : threadIdx.x;
+    const int wide = FEW ? 64 : 1 << a.width, parts = FEW ? 1 : kFinishThreads >> a.width;
+    const int lane = tid & (wide - 1), r = FEW ? 0 : tid >> a.width;
+    const uint32_t tile = FEW ? blockIdx.x * (kFewThreads / 64) + (threadIdx.x >> 6) : blockIdx.x;
+    if (FEW && tile >= a.all_tiles) return;
+    const int64_t n = tile / static_cast<uint32_t>(a.tiles);
+    const int c = static_cast<int>(tile % static_cast<uint32_t>(a.tiles)) * a.tile_c + lane;
     const bool live = lane < a.tile_c && c < a.C;
     double s1 = 0.0, s2 = 0.0;
     float ga[1] = {0.0f}, rs = 0.0f;
@@ -321,8 +327,8 @@ __global__ __launch_bounds__(kFinishThreads) void gn_grad_finish(FinishArgs a) {
         rs = a.rstd[n * a.G + c / a.Cg];
         load_affine<1>(a.af.gamma, a.af.type, c, 1.0f, ga);
         const float *p = a.part + n * a.K * 2 * a.C + c;
-        // eight partials' loads in flight (the last ones clamped, not added)
-        constexpr int kBatch = 8;
+        // the loads of a batch in flight (the last ones clamped, not added)
+        constexpr int kBatch = kFinishBatch;
         const int64_t step = 2 * static_cast<int64_t>(a.C);
         for (int64_t k = r; k < a.K; k += kBatch * parts) {
             float v1[kBatch], v2[kBatch];
@@ -340,28 +346,31 @@ __global__ __launch_bounds__(kFinishThreads) void gn_grad_finish(FinishArgs a) {
             }
         }
     }
-    // the parts within a wave by a butterfly, then the 16 waves' sums: wave 0
-    // adds each channel's in `per` interleaved runs and joins those
-    const int per = 64 >> a.width;
-    for (int o = wide; o < 64; o <<= 1) {
-        s1 += __shfl_xor(s1, o, 64);
-        s2 += __shfl_xor(s2, o, 64);
-    }
-    if ((tid & 63) < wide) {
-        red[0][(tid >> 6) * wide + lane] = s1;
-        red[1][(tid >> 6) * wide + lane] = s2;
-    }
-    __syncthreads();
-    if (tid >= 64) return;
-    s1 = s2 = 0.0;
+    if constexpr (!FEW) {
+        // the parts within a wave by a butterfly, then the 16 waves' sums: wave
+        // 0 adds each channel's in `per` interleaved runs and joins those
+        __shared__ double red[2][kFinishThreads];
+        const int per = 64 >> a.width;
+        for (int o = wide; o < 64; o <<= 1) {
+            s1 += __shfl_xor(s1, o, 64);
+            s2 += __shfl_xor(s2, o, 64);
+        }
+        if ((tid & 63) < wide) {
+            red[0][(tid >> 6) * wide + lane] = s1;
+            red[1][(tid >> 6) * wide + lane] = s2;
+        }
+        __syncthreads();
+        if (tid >= 64) return;
+        s1 = s2 = 0.0;
 #pragma unroll 4
-    for (int w = r; w < kFinishThreads / 64; w += per) {
-        s1 += red[0][w * wide + lane];
-        s2 += red[1][w * wide + lane];
-    }
-    for (int o = wide; o < 64; o <<= 1) {
-        s1 += __shfl_xor(s1, o, 64);
-        s2 += __shfl_xor(s2, o, 64);
+        for (int w = r; w < kFinishThreads / 64; w += per) {
+            s1 += red[0][w * wide + lane];
+            s2 += red[1][w * wide + lane];
+        }
+        for (int o = wide; o < 64; o <<= 1) {
+            s1 += __shfl_xor(s1, o, 64);
+            s2 += __shfl_xor(s2, o, 64);
+        }
     }
     s2 *= static_cast<double>(rs);
     if (live && r == 0) {
@@ -373,10 +382,18 @@ __global__ __launch_bounds__(kFinishThreads) void gn_grad_finish(FinishArgs a) {
     if (a.coef == nullptr) return;
     s1 *= static_cast<double>(ga[0]);
     s2 *= static_cast<double>(ga[0]);
+    // The sums of lanes lane .. lane + Cg - 1, the group that starts at the
+    // lane, from runs of 1, 2, 4, ... lanes (a group of 64 lanes, lane by lane:
+    // 677 us at (8192,1,2048) with 64 channels a group).
     double ta = 0.0, tb = 0.0;
-    for (int i = 0; i < a.Cg; ++i) {  // lanes lane .. lane + Cg - 1: the lane's group
-        ta += __shfl(s1, lane + i, 64);
-        tb += __shfl(s2, lane + i, 64);
+    for (int run = 1, at = lane; run <= a.Cg; run <<= 1) {
+        if (a.Cg & run) {
+            ta += __shfl(s1, at, 64);
+            tb += __shfl(s2, at, 64);
+            at += run;
+        }
+        s1 += __shfl(s1, lane + run, 64);
+        s2 += __shfl(s2, lane + run, 64);
     }
     if (live && r == 0 && lane % a.Cg == 0) {
         float *o = a.coef + 2 * (n * a.G + c / a.Cg);
@@ -419,8 +436,8 @@ __global__ __launch_bounds__(kLanes) void gn_grad_groups(FinishArgs a) {
 // dgamma and dbeta of N samples (zeros for none): a workgroup takes 16 channels
 // and 16 parts of the samples, each part's in order with eight samples' loads
 // in flight, then the parts in a fixed order, in fp64.  One lane a channel, a
-// sample at a time, took 0.27 us a sample: (10000,64,64) 2855 us, 490 so,
-// (2000,256,64) 605 and 132, (128,64,16) 38 and 25.
+// sample at a time, took 0.27 us a sample: 72.5 us of pass 2's launch at
+// (300,3,32), 5.6 so.
 constexpr int kSampleLanes = 16, kSampleParts = kLanes / kSampleLanes;
 __device__ __forceinline__ void add_samples(const float *sums, int64_t N, int C, int block,
                                             void *dgamma, void *dbeta, int type) {
@@ -478,13 +495,13 @@ __global__ __launch_bounds__(kLanes) void gn_grad_samples(const float *sums, int
 template <class D, int W, bool TAIL, bool SILU, bool SAVED>
 __global__ __launch_bounds__(kLanes) void gn_grad_input(RowArgs a) {
     using T = typename D::storage;
-    if (blockIdx.x >= a.rows_end) {
-        add_samples(a.sums, a.N, a.tl.C, static_cast<int>(blockIdx.x - a.rows_end), a.dgamma,
-                    a.dbeta, a.af.type);
+    if (blockIdx.x < a.sample_blocks) {
+        add_samples(a.sums, a.N, a.tl.C, static_cast<int>(blockIdx.x), a.dgamma, a.dbeta,
+                    a.af.type);
         return;
     }
     const Tiles &tl = a.tl;
-    const Place<W, TAIL> at(tl);
+    const Place<W, TAIL> at(tl, blockIdx.x - a.sample_blocks);
     const int64_t row0 = at.n * tl.L + at.r;
     using V = Pair<D, W, TAIL, SAVED>;
     const typename V::From from(a, row0, at.c);
@@ -936,6 +953,7 @@ struct BackwardPlan {
     StripPlan strip;
     Tiles sums, input;
     int lanes;  // of pass 1's workgroups
+    bool few;   // partials
     int tile_c, tiles, width;
     size_t part, total;  // floats
 };
@@ -947,12 +965,15 @@ BackwardPlan backward_plan(int64_t N, int64_t L, int64_t C, int64_t G, int dtype
         p.total = N > 1 ? static_cast<size_t>(N) * 2 * C : 0;
         return p;
     }
-    p.lanes = N * L * C * elem_bytes(dtype) <= kSmallBytes ? kLanes : kSumLanes;
+    const bool small = N * L * C * elem_bytes(dtype) <= kSmallBytes;
+    const bool one_batch = L * std::min<int64_t>(ceil_div(C, w), kMaxPieces) <= kLanes * kUnroll;
+    p.lanes = small || one_batch ? kLanes : kSumLanes;
     p.sums = make_tiles(N, L, C, w, 1, kSumBlocks, kMaxRun, p.lanes);
     p.input = make_tiles(N, L, C, w, 1, kStreamBlocks, 0, kLanes,
                          saved ? kUnroll : kInputUnroll);
     const int64_t cg = C / G;
-    p.width = cg <= 16 || cg > 64 ? 4 : (cg <= 32 ? 5 : 6);
+    p.few = p.sums.K <= kFinishBatch;
+    p.width = p.few ? 6 : (cg <= 16 || cg > 64 ? 4 : (cg <= 32 ? 5 : 6));
     const int64_t wide = int64_t{1} << p.width;
     p.tile_c = static_cast<int>(cg <= 64 ? wide / cg * cg : wide);
     p.tiles = static_cast<int>(ceil_div(C, p.tile_c));
@@ -1197,6 +1218,7 @@ gn_status gn_silu_rows_backward(const void *dy, const void *x, const void *codes
     f.Cg = a.Cg;
     f.tile_c = p.tile_c;
     f.tiles = p.tiles;
+    f.all_tiles = N * p.tiles;
     f.width = p.width;
     f.inv_m = 1.0 / (static_cast<double>(L) * static_cast<double>(a.Cg));
     f.af = a.af;
@@ -1237,8 +1259,12 @@ gn_status gn_silu_rows_backward(const void *dy, const void *x, const void *codes
             else
                 gn_grad_sums<D, W, TAIL, SILU, SAVED, kSumLanes>
                     <<<grid_of(N, a.tl), kSumLanes, 0, c.stream>>>(a);
-            gn_grad_finish<<<dim3(static_cast<unsigned>(N * p.tiles)), kFinishThreads, 0, c.stream>>>(
-                f);
+            const int64_t per = p.few ? kFewThreads / 64 : 1;
+            const unsigned tiles = static_cast<unsigned>(ceil_div(f.all_tiles, per));
+            if (p.few)
+                gn_grad_finish<true><<<tiles, kFewThreads, 0, c.stream>>>(f);
+            else
+                gn_grad_finish<false><<<tiles, kFinishThreads, 0, c.stream>>>(f);
             if (f.coef == nullptr) {
                 FinishArgs g = f;
                 g.coef = coef;
@@ -1246,8 +1272,8 @@ gn_status gn_silu_rows_backward(const void *dy, const void *x, const void *codes
             }
             a.tl = p.input;
             dim3 grid = grid_of(N, a.tl);
-            a.rows_end = grid.x;
-            if (grads && N > 1) grid.x += sgrid;
+            a.sample_blocks = grads && N > 1 ? sgrid : 0;
+            grid.x += a.sample_blocks;
             gn_grad_input<D, W, TAIL, SILU, SAVED><<<grid, kLanes, 0, c.stream>>>(a);
         };
         auto by_saved = [&](auto silu) {

@@ -108,7 +108,11 @@ def test_rows_saved_and_restored(gn, M, C, dtype):
 @pytest.mark.parametrize("shape,dtype", [
     ((2, 9, 24, 3), BF16), ((17, 3, 24, 3), FP32), ((128, 5, 64, 1), BF16), ((129, 5, 64, 1), FP16),
     ((255, 2, 32, 1), FP32), ((257, 3, 40, 8), BF16), ((1025, 9, 33, 3), FP32),
-    ((3000, 16, 64, 8), BF16), ((1100, 3, 7, 7), FP16), ((600, 2, 200, 2), BF16)])
+    ((3000, 16, 64, 8), BF16), ((1100, 3, 7, 7), FP16), ((600, 2, 200, 2), BF16),
+    # a wave's tile of a few partials: groups of 1 to 64 channels, and beyond
+    ((30, 3, 96, 96), BF16), ((200, 3, 2048, 1), BF16), ((64, 1, 2048, 32), FP16),
+    ((70, 4, 640, 32), BF16), ((40, 5, 1000, 25), FP32), ((30, 70, 330, 10), BF16),
+    ((60, 2, 4092, 66), FP32), ((50, 700, 252, 4), BF16), ((9, 999, 1001, 7), FP16)])
 def test_weight_gradients_of_many_samples(gn, shape, dtype, saved):
     """Samples on both sides of a round of the sum over samples (128), in the
     single launch (up to 256) and behind the passes."""
