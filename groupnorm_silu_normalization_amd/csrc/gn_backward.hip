@@ -24,10 +24,10 @@
 // (gn_grad_strip).
 //
 // Measured on MI355X, bf16 (a 1 GiB copy reads and writes 5.1 TB/s there):
-// (1,1048576,256) pass 1 191 us (5.6 TB/s, VALU 77% busy), finish 5.8 us, pass
-// 2 284 us (5.7 TB/s); from the checkpoint, (1,65536,512), 28.9, 6.0 and 31.7
+// (1,1048576,256) pass 1 191 us (5.6 TB/s, VALU 76% busy), finish 5.8 us, pass
+// 2 284 us (5.7 TB/s); from the checkpoint, (1,65536,512), 28.7, 5.6 and 31.5
 // us (pass 1 bound by the VALU and its start and end, pass 2 by its stores);
-// apply that saves, (1,262144,512), 130 us (5.2 TB/s), restored 71.5 us (5.7).
+// apply that saves, (1,262144,512), 130 us (5.2 TB/s), restored 71.6 us (5.7).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -547,7 +547,7 @@ __global__ __launch_bounds__(kLanes) void gn_grad_input(RowArgs a) {
 // dx is stored through the L2: strips narrower than a cache line write parts
 // of lines, which neighbouring strips on the same XCD complete there
 // ((1,4096,128): 22.0 us of kernel time with nontemporal stores and strips
-// dealt over the XCDs, 16.8 so).
+// dealt over the XCDs, 16.7 so).
 constexpr int kStripLanes = 1024;
 constexpr int kStripMaxPieces = 4;    // NP
 constexpr int kStripMaxRow = 128;     // P

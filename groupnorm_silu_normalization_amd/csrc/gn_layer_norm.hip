@@ -30,10 +30,10 @@
 // (in fp64) in a fixed order: no atomics, the same bits on every call.
 //
 // Measured on MI355X, bf16 (a 1 GiB copy reads and writes 5.1 TB/s there):
-// (16384,4096) forward 45.9 us (5.85 TB/s), backward 77.8 us (5.3 TB/s) and
-// column sums 5.0 us; forward with the checkpoint (8192,2560) 23.7 us; backward
-// from the checkpoint (5001,1537) 16.0 us (five rows a slot: their latencies
-// and the sums' instructions bound it) and 3.9 us.
+// (16384,4096) forward 45.9 us (5.85 TB/s), backward 78.3 us (5.25 TB/s) and
+// column sums 4.8 us; forward with the checkpoint (8192,2560) 22.4 us; backward
+// from the checkpoint (5001,1537) 16.2 us (five rows a slot: their latencies
+// and the sums' instructions bound it) and 3.8 us.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
