@@ -15,9 +15,12 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libgnsilu.so")
-SOURCES = [os.path.join(CSRC, f) for f in ("gn_api.hip", "gn_backward.hip", "gn_layer_norm.hip")]
+SOURCES = [os.path.join(CSRC, f) for f in ("gn_api.hip", "gn_backward.hip", "gn_layer_norm.hip",
+                                             "gn_rms_norm.hip", "gn_rows8.hip",
+                                             "gn_int8_matmul.hip")]
 DEPENDS = SOURCES + [os.path.join(CSRC, f) for f in ("gn_conv.hpp", "gn_host.hpp", "gn_kernels.hpp",
-                                                     "gn_rows.hpp", "gn_types.hpp")]
+                                                     "gn_row_passes.hpp", "gn_rows.hpp", "gn_rows8.hpp",
+                                                     "gn_types.hpp")]
 DEPENDS.append(os.path.join(INCLUDE, "gnsilu.h"))
 ARCH = "gfx950"
 

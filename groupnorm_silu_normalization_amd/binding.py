@@ -29,13 +29,19 @@ group_norm_silu_rows_backward (after group_stats_rows and apply_rows), and
 and apply_rows).  Like the rest they run with autograd disabled, i.e. inside a
 torch.autograd.Function.
 
+For language models: rms_norm_rows (with the residual's addition, and an output
+in 8 bits) and rms_norm_rows_backward; rows in 8 bits with a scale each
+(quantize_rows, dequantize_rows, Rows8) and their matrix product
+(pack_int8_weight, int8_matmul).
+
 The raw C entry points are re-exported under their C names (gn_silu_nhwc,
 gn_silu_rows, gn_silu_nhwc_strided, gn_silu_ndhwc, gn_stats_rows,
 gn_apply_rows, gn_profile_rows, gn_plan_rows, their *_dtype forms,
 gn_silu_rows_noalloc, gn_layer_norm_rows and gn_layer_norm_rows_backward,
 gn_silu_rows_backward, gn_apply_rows_save, gn_checkpoint_rows,
-gn_restore_rows, gn_kernel_name, gn_status_string, gn_version,
-gn_device_info).
+gn_restore_rows, gn_rms_norm_rows and gn_rms_norm_rows_backward,
+gn_quantize_rows, gn_dequantize_rows, gn_int8_pack_weights, gn_int8_matmul,
+gn_kernel_name, gn_status_string, gn_version, gn_device_info).
 """
 import ctypes
 import enum
@@ -130,6 +136,18 @@ lib.gn_apply_rows_save.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64,
 lib.gn_silu_rows_backward_workspace.argtypes = [_i64, _i64, _i64, _i64, _int, _i64p]
 lib.gn_silu_rows_backward.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64,
                                       _i64, _i64, _i64, _int, _int, _vp, _i64, _vp]
+lib.gn_quantize_rows.argtypes = [_vp, _i64, _vp, _i64, _vp, _i64, _i64, _int, _vp]
+lib.gn_dequantize_rows.argtypes = [_vp, _i64, _vp, _vp, _i64, _i64, _i64, _int, _vp]
+lib.gn_rms_norm_rows.argtypes = [_vp, _i64, _vp, _i64, _vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp,
+                                 _vp, _i64, _i64, _f32, _int, _vp]
+lib.gn_rms_norm_rows_backward_workspace.argtypes = [_i64, _i64, _int, _i64p]
+lib.gn_rms_norm_rows_backward.argtypes = [_vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _vp,
+                                          _i64, _vp, _i64, _i64, _int, _vp, _i64, _vp]
+lib.gn_int8_packed_bytes.argtypes = [_i64, _i64, _i64p]
+lib.gn_int8_pack_weights.argtypes = [_vp, _i64, _vp, _i64, _i64, _vp]
+lib.gn_int8_matmul_workspace.argtypes = [_i64, _i64, _i64, _int, _i64p]
+lib.gn_int8_matmul.argtypes = [_vp, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _vp, _i64, _i64, _i64,
+                               _i64, _int, _vp, _i64, _vp]
 lib.gn_plan_rows_dtype.argtypes = [_i64, _i64, _i64, _i64, _int, _i64p]
 lib.gn_plan_single_launch.argtypes = [_i64, _i64, _i64, _i64, _int, _i64p]
 for _name in ("gn_silu_nhwc", "gn_silu_rows", "gn_silu_nhwc_strided", "gn_stats_rows",
@@ -141,7 +159,11 @@ for _name in ("gn_silu_nhwc", "gn_silu_rows", "gn_silu_nhwc_strided", "gn_stats_
               "gn_silu_rows_noalloc", "gn_plan_single_launch", "gn_noalloc_scratch",
               "gn_checkpoint_rows", "gn_restore_rows", "gn_layer_norm_rows",
               "gn_layer_norm_rows_backward_workspace", "gn_layer_norm_rows_backward",
-              "gn_apply_rows_save", "gn_silu_rows_backward_workspace", "gn_silu_rows_backward"):
+              "gn_apply_rows_save", "gn_silu_rows_backward_workspace", "gn_silu_rows_backward",
+              "gn_quantize_rows", "gn_dequantize_rows", "gn_rms_norm_rows",
+              "gn_rms_norm_rows_backward_workspace", "gn_rms_norm_rows_backward",
+              "gn_int8_packed_bytes", "gn_int8_pack_weights", "gn_int8_matmul_workspace",
+              "gn_int8_matmul"):
     getattr(lib, _name).restype = _int
 lib.gn_plan_rows.argtypes = [_i64, _i64, _i64, _i64, _i64p]
 lib.gn_plan_rows.restype = _int
@@ -188,6 +210,15 @@ gn_layer_norm_rows_backward = lib.gn_layer_norm_rows_backward
 gn_apply_rows_save = lib.gn_apply_rows_save
 gn_silu_rows_backward_workspace = lib.gn_silu_rows_backward_workspace
 gn_silu_rows_backward = lib.gn_silu_rows_backward
+gn_quantize_rows = lib.gn_quantize_rows
+gn_dequantize_rows = lib.gn_dequantize_rows
+gn_rms_norm_rows = lib.gn_rms_norm_rows
+gn_rms_norm_rows_backward_workspace = lib.gn_rms_norm_rows_backward_workspace
+gn_rms_norm_rows_backward = lib.gn_rms_norm_rows_backward
+gn_int8_packed_bytes = lib.gn_int8_packed_bytes
+gn_int8_pack_weights = lib.gn_int8_pack_weights
+gn_int8_matmul_workspace = lib.gn_int8_matmul_workspace
+gn_int8_matmul = lib.gn_int8_matmul
 gn_status_string = lib.gn_status_string
 gn_version = lib.gn_version
 gn_device_info = lib.gn_device_info
@@ -196,6 +227,9 @@ MAX_CHANNELS = 8192
 NOALLOC_SCRATCH_BYTES = 1 << 20   # GN_NOALLOC_SCRATCH_BYTES
 LAYER_NORM_MAX_CHANNELS = 16384   # GN_LAYER_NORM_MAX_CHANNELS
 CHECKPOINT_BLOCK = 32             # GN_CHECKPOINT_BLOCK
+INT8_MAX_K = 65536                # GN_INT8_MAX_K
+INT8_MAX_N = 1 << 20              # GN_INT8_MAX_N
+INT8_MAX_M = 1 << 20              # GN_INT8_MAX_M
 
 
 class GnDtype(enum.IntEnum):
@@ -784,6 +818,314 @@ def group_norm_silu_rows_backward(dy, x, mean, rstd, weight=None, bias=None, app
         _addr(weight), _addr(bias), _addr(out), _addr(dw), _addr(db), N, L, C, G,
         1 if apply_silu else 0, dtype, _addr(ws), size)
     return _result(code, (out, dw, db))
+
+
+class Rows8:
+    """Rows in 8 bits with a scale each (the format in gnsilu.h): ``codes``
+    int8 (..., C), its rows evenly spaced, ``scales`` fp32 (...), contiguous,
+    and the ``dtype`` of the rows that they stand for.  The library's own rows
+    start 16 bytes apart or a multiple of that, which is what ``int8_matmul``
+    reads without a copy."""
+
+    def __init__(self, codes, scales, dtype):
+        torch = _torch()
+        if not isinstance(codes, torch.Tensor) or not isinstance(scales, torch.Tensor):
+            raise TypeError("codes and scales must be tensors")
+        if codes.dtype != torch.int8 or scales.dtype != torch.float32:
+            raise TypeError("8-bit rows hold int8 codes and fp32 scales")
+        if codes.dim() < 1 or scales.shape != codes.shape[:-1]:
+            raise ValueError("scales must have shape codes.shape[:-1]")
+        if dtype_code(dtype) is None:
+            raise TypeError("unsupported dtype %s" % dtype)
+        if codes.device != scales.device:
+            raise ValueError("codes and scales must be on one device")
+        if _row_stride(codes) is None or not scales.is_contiguous():
+            raise ValueError("the rows of codes must be evenly spaced, scales contiguous")
+        self.codes, self.scales, self.dtype = codes, scales, dtype
+
+    shape = property(lambda self: self.codes.shape)
+    device = property(lambda self: self.codes.device)
+
+
+def _empty_rows8(x):
+    """Unwritten 8-bit rows of x's shape (of a supported dtype), made without
+    __init__'s checks, and the distance of their rows."""
+    torch = _torch()
+    C = x.shape[-1]
+    step = (C + 15) & ~15
+    q = Rows8.__new__(Rows8)
+    if step == C:
+        q.codes = torch.empty(x.shape, dtype=torch.int8, device=x.device)
+    else:
+        q.codes = torch.empty(x.shape[:-1] + (step,), dtype=torch.int8, device=x.device)[..., :C]
+    q.scales = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    q.dtype = x.dtype
+    return q, step
+
+
+def quantize_rows(x):
+    """The rows x[..., :] in 8 bits with a scale each (a Rows8), or None when
+    the library declines x."""
+    if not _gpu_rows(x):
+        return None
+    C, step = x.shape[-1], _row_stride(x)
+    if step is None or C == 0 or C > LAYER_NORM_MAX_CHANNELS:
+        return None
+    q, qstep = _empty_rows8(x)
+    if not x.numel():
+        return q
+    code = _run(lib.gn_quantize_rows, x, _addr(x), step, _addr(q.codes), qstep, _addr(q.scales),
+                _rows_of(x), C, dtype_code(x.dtype))
+    return _result(code, q)
+
+
+def dequantize_rows(rows, dtype=None, out=None):
+    """The rows that a Rows8 stands for, in ``dtype`` (by default the type they
+    were made from); None when the library declines them."""
+    torch = _torch()
+    if not isinstance(rows, Rows8):
+        raise TypeError("dequantize_rows takes a Rows8")
+    codes = rows.codes
+    C = codes.shape[-1]
+    if (codes.device.type != "cuda" or torch.is_grad_enabled() or C == 0
+            or C > LAYER_NORM_MAX_CHANNELS):
+        return None
+    if out is None:
+        dtype = rows.dtype if dtype is None else dtype
+        if dtype_code(dtype) is None:
+            raise TypeError("unsupported dtype %s" % dtype)
+        out = torch.empty(codes.shape, dtype=dtype, device=codes.device)
+    elif (out.shape != codes.shape or out.device != codes.device
+          or dtype_code(out.dtype) is None or (dtype is not None and out.dtype != dtype)):
+        raise ValueError("out must match in shape, dtype and device")
+    step = _row_stride(out)
+    if step is None:
+        return None
+    if not out.numel():
+        return out
+    code = _run(lib.gn_dequantize_rows, codes, _addr(codes), _row_stride(codes),
+                _addr(rows.scales), _addr(out), step, _rows_of(codes), C, dtype_code(out.dtype))
+    return _result(code, out)
+
+
+def rms_norm_rows(x, weight=None, eps=1e-6, *, residual=None, quantize=False, stats=False,
+                  out=None, residual_out=None):
+    """Root-mean-square norm of the rows h[..., :] over their C values, where
+    h = x + residual rounded to x's type (h = x without a residual).
+
+    x, residual: bf16, fp16 or fp32, of one shape and type; rows evenly spaced,
+    C <= LAYER_NORM_MAX_CHANNELS.  weight: C values in fp32, bf16 or fp16, or
+    None.  ``quantize``: y comes in 8 bits (a Rows8, for ``int8_matmul``)
+    instead of x's type.  Returns y; with a residual or ``stats`` the tuple
+    (y, h, rstd) of those that were asked for, rstd fp32 of shape x.shape[:-1].
+    ``out`` takes y (not with ``quantize``), ``residual_out`` takes h; they may
+    be x or residual themselves.  None when the library declines the input."""
+    torch = _torch()
+    if not _gpu_rows(x):
+        return None
+    C = x.shape[-1]
+    if residual is not None:
+        if not isinstance(residual, torch.Tensor):
+            raise TypeError("residual must be a tensor or None")
+        if residual.shape != x.shape:
+            raise ValueError("residual must have x's shape")
+        if residual.dtype != x.dtype or residual.device != x.device:
+            return None
+    elif residual_out is not None:
+        raise ValueError("residual_out needs a residual")
+    if quantize and out is not None:
+        raise ValueError("out takes no 8-bit rows")
+    if not _affine_ok(weight, C, x.device, "weight"):
+        return None
+    step = _row_stride(x)
+    rstep = C if residual is None else _row_stride(residual)
+    if step is None or rstep is None or C == 0 or C > LAYER_NORM_MAX_CHANNELS:
+        return None
+    y = q = h = rstd = None
+    ystep = qstep = hstep = C
+    if quantize:
+        q, qstep = _empty_rows8(x)
+    elif out is None:
+        y = _dense_like(x)
+    else:
+        _check_out(out, x)
+        y, ystep = out, _row_stride(out)
+    if residual_out is not None:
+        _check_out(residual_out, x)
+        h, hstep = residual_out, _row_stride(residual_out)
+    elif residual is not None:
+        h = _dense_like(x)
+    if ystep is None or hstep is None:
+        return None
+    if stats:
+        rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    r = q if quantize else y
+    if residual is not None or stats:
+        r = (r,) + ((h,) if residual is not None else ()) + ((rstd,) if stats else ())
+    if not x.numel():
+        return r
+    code = _run(
+        lib.gn_rms_norm_rows, x, _addr(x), step, _addr(residual), rstep, _addr(weight), _addr(h),
+        hstep, _addr(y), ystep, _addr(q.codes) if q else None, qstep,
+        _addr(q.scales) if q else None, _addr(rstd), _rows_of(x), C, float(eps),
+        dtype_code(x.dtype) | _affine_flag(weight, None))
+    return _result(code, r)
+
+
+def rms_norm_rows_backward(dy, x, rstd, weight=None, *, residual_grad=None, weight_grad=True,
+                           out=None):
+    """Backward pass of ``rms_norm_rows``: (dx, dweight).
+
+    x: the rows that were normalised (h where the forward pass added a
+    residual), or their Checkpoint8; rstd: as the forward pass returned it.
+    ``residual_grad``: the gradient that reaches h past the norm, added to dx.
+    The forward pass's x and residual both have the gradient dx.  dweight has
+    weight's type (fp32 without a weight), and is None unless ``weight_grad``.
+    None when the library declines the input."""
+    torch = _torch()
+    if not _gpu_rows(dy, "dy"):
+        return None
+    C, M = dy.shape[-1], _rows_of(dy)
+    ok, xp, codes, scales = _saved_input(x, dy)
+    ok = _stat(rstd, M, "rstd", dy) and ok
+    ok = _affine_ok(weight, C, dy.device, "weight") and ok
+    if residual_grad is not None:
+        if not isinstance(residual_grad, torch.Tensor):
+            raise TypeError("residual_grad must be a tensor or None")
+        if residual_grad.shape != dy.shape:
+            raise ValueError("residual_grad must have dy's shape")
+        ok = residual_grad.dtype == dy.dtype and residual_grad.device == dy.device and ok
+    if not ok or C == 0 or C > LAYER_NORM_MAX_CHANNELS:
+        return None
+    step = _row_stride(dy)
+    xstep = C if xp is None else _row_stride(x)
+    hstep = C if residual_grad is None else _row_stride(residual_grad)
+    if step is None or xstep is None or hstep is None:
+        return None
+    if out is None:
+        out = _dense_like(dy)
+        ostep = C
+    else:
+        _check_out(out, dy)
+        ostep = _row_stride(out)
+        if ostep is None:
+            return None
+    dw = None
+    if weight_grad:
+        dw = torch.empty(C, dtype=torch.float32 if weight is None else weight.dtype,
+                         device=dy.device)
+    if M == 0:
+        if weight_grad:
+            dw.zero_()
+        return out, dw
+    dtype = dtype_code(dy.dtype) | _affine_flag(weight, None)
+    ws, size = None, 0
+    if weight_grad:
+        size = _workspace_bytes("gn_rms_norm_rows_backward_workspace", M, C, dtype)
+        if size is None:
+            return None
+        if size:
+            ws = torch.empty(size, dtype=torch.uint8, device=dy.device)
+    code = _run(
+        lib.gn_rms_norm_rows_backward, dy, _addr(dy), step, xp, xstep, codes, scales, _addr(rstd),
+        _addr(weight), _addr(residual_grad), hstep, _addr(out), ostep, _addr(dw), M, C, dtype,
+        _addr(ws), size)
+    return _result(code, (out, dw))
+
+
+class PackedInt8Weight:
+    """An (N, K) weight in 8 bits packed once into the library's fragment order
+    (gn_int8_pack_weights), with its scales, for repeated products."""
+
+    def __init__(self, data, scales, N, K):
+        self.data, self.scales, self.shape = data, scales, (N, K)
+        self.device = data.device
+
+
+def pack_int8_weight(weight):
+    """Packs a Rows8 of shape (N, K), one row and scale for each output channel
+    (``quantize_rows`` of the weight); None if declined."""
+    torch = _torch()
+    if not isinstance(weight, Rows8):
+        raise TypeError("pack_int8_weight takes a Rows8")
+    if weight.codes.dim() != 2:
+        raise ValueError("the weight must have shape (N, K)")
+    N, K = weight.shape
+    if weight.device.type != "cuda" or torch.version.hip is None:
+        return None
+    size = _workspace_bytes("gn_int8_packed_bytes", N, K)
+    if size is None:
+        return None
+    data = torch.empty(size, dtype=torch.int8, device=weight.device)
+    code = _run(lib.gn_int8_pack_weights, weight.codes, _addr(weight.codes),
+                _row_stride(weight.codes), _addr(data), N, K)
+    return _result(code, PackedInt8Weight(data, weight.scales, N, K))
+
+
+def int8_matmul(x, weight, bias=None, *, residual=None, dtype=None, out=None):
+    """z[..., n] = sum_k x[..., k] * weight[n, k] + bias[n] + residual[..., n] of
+    rows and weights in 8 bits: exact integer sums, scaled in fp32, rounded
+    once to ``dtype`` (by default the type that x stands for).
+
+    x: a Rows8 of shape (..., K) (``rms_norm_rows(quantize=True)``,
+    ``quantize_rows``); weight: a PackedInt8Weight of shape (N, K), or a Rows8,
+    which is packed in the call; bias: N values in fp32, bf16 or fp16, or None;
+    residual: (..., N) of z's type with evenly spaced rows, or None; ``out``
+    may be residual.  None when the library declines the input."""
+    torch = _torch()
+    if not isinstance(x, Rows8):
+        raise TypeError("x must be a Rows8")
+    if not isinstance(weight, (PackedInt8Weight, Rows8)):
+        raise TypeError("weight must be a PackedInt8Weight or a Rows8")
+    codes = x.codes
+    K = codes.shape[-1]
+    if len(weight.shape) != 2 or weight.shape[1] != K:
+        raise ValueError("weight must have shape (N, %d)" % K)
+    N = weight.shape[0]
+    shape = codes.shape[:-1] + (N,)
+    dtype = x.dtype if dtype is None else dtype
+    if dtype_code(dtype) is None:
+        raise TypeError("unsupported dtype %s" % dtype)
+    if (codes.device.type != "cuda" or torch.version.hip is None or torch.is_grad_enabled()
+            or weight.device != codes.device or not 0 < K <= INT8_MAX_K or not 0 < N <= INT8_MAX_N):
+        return None
+    if not _affine_ok(bias, N, codes.device, "bias"):
+        return None
+    rstep = zstep = N
+    if residual is not None:
+        if not isinstance(residual, torch.Tensor):
+            raise TypeError("residual must be a tensor or None")
+        if residual.shape != shape:
+            raise ValueError("residual must have shape %s" % (tuple(shape),))
+        rstep = _row_stride(residual)
+        if residual.dtype != dtype or residual.device != codes.device or rstep is None:
+            return None
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=codes.device)
+    else:
+        if out.shape != shape or out.dtype != dtype or out.device != codes.device:
+            raise ValueError("out must match in shape, dtype and device")
+        zstep = _row_stride(out)
+        if zstep is None:
+            return None
+    M = _rows_of(codes)
+    if M == 0:
+        return out
+    if isinstance(weight, Rows8):
+        weight = pack_int8_weight(weight)
+        if weight is None:
+            return None
+    step = _row_stride(codes)
+    aligned = 1 if (M == 1 or step % 16 == 0) and codes.data_ptr() % 16 == 0 else 0
+    size = _workspace_bytes("gn_int8_matmul_workspace", M, N, K, aligned)
+    if size is None:
+        return None
+    ws = torch.empty(size, dtype=torch.uint8, device=codes.device) if size else None
+    code = _run(
+        lib.gn_int8_matmul, codes, _addr(codes), step, _addr(x.scales), _addr(weight.data),
+        _addr(weight.scales), _addr(bias), _addr(residual), rstep, _addr(out), zstep, M, N, K,
+        dtype_code(dtype) | _affine_flag(bias, None), _addr(ws), size)
+    return _result(code, out)
 
 
 PLAN_FIELDS = ("slots", "tiles", "full", "tpc1", "K1", "tpc2", "K2", "scratch_bytes",

@@ -56,6 +56,14 @@ template <class D> struct Piece16x8 {
         else
             *reinterpret_cast<u32x4_a2 *>(p) = v;
     }
+    // values rounded to the type, and stored as they are held
+    __device__ __forceinline__ void set(const float (&o)[8]) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = D::pack2(o[2 * j], o[2 * j + 1]);
+    }
+    __device__ __forceinline__ void put(uint16_t *p) const {
+        *reinterpret_cast<u32x4_a2 *>(p) = w;
+    }
 };
 template <> struct Piece<Bf16, 8> : Piece16x8<Bf16> {};
 template <> struct Piece<Fp16, 8> : Piece16x8<Fp16> {};
@@ -81,6 +89,11 @@ template <> struct Piece<F32, 4> {
         else
             *reinterpret_cast<u32x4_a4 *>(p) = v;
     }
+    __device__ __forceinline__ void set(const float (&o)[4]) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = __float_as_uint(o[j]);
+    }
+    __device__ __forceinline__ void put(float *p) const { *reinterpret_cast<u32x4_a4 *>(p) = w; }
 };
 
 template <class D> struct Piece<D, 1> {
@@ -93,6 +106,8 @@ template <class D> struct Piece<D, 1> {
     __device__ __forceinline__ static void store(typename D::storage *p, const float (&o)[1]) {
         st<NT>(p, D::from_f32(o[0]));
     }
+    __device__ __forceinline__ void set(const float (&o)[1]) { b = D::from_f32(o[0]); }
+    __device__ __forceinline__ void put(typename D::storage *p) const { *p = b; }
 };
 
 // Stores the channels j >= lo of a piece one by one (the last piece of a row

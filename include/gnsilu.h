@@ -444,6 +444,89 @@ gn_status gn_silu_rows_backward(const void *dy, const void *x, const void *codes
                                 int apply_silu, int dtype, void *workspace,
                                 int64_t workspace_bytes, void *stream);
 
+/* Root-mean-square norm, rows in 8 bits and their matrix product ----------------
+ *
+ * The conventions of the section above hold here too: element alignment, row
+ * strides, the caller's workspace, aliasing of an output with an input of the
+ * same stride (y == x, h == x or h == residual, dx == dy, x or dh).  C is at
+ * most GN_LAYER_NORM_MAX_CHANNELS.
+ *
+ * Rows in 8 bits.  A row t of C values is kept as int8 codes with one fp32
+ * scale,
+ *     q[c] = round_half_even(127 * t[c] / max|t|),  scale = max|t| / 127,
+ * and stands for q * scale.  The codes are those of the exact quotient of the
+ * row's fp32 values, whatever kernel writes them.  A row of zeros has codes 0
+ * (and scale 0), a row that holds an infinity or a NaN has codes 0 and the
+ * scale NaN: it stands for NaN throughout.  codes: int8, row m at
+ * m * codes_stride (codes_stride >= C where M > 1; what lies between the rows
+ * is left as it was), any alignment; scales: fp32 [M]. */
+gn_status gn_quantize_rows(const void *x, int64_t x_stride, void *codes, int64_t codes_stride,
+                           float *scales, int64_t M, int64_t C, int dtype, void *stream);
+/* q * scale, rounded once to dtype. */
+gn_status gn_dequantize_rows(const void *codes, int64_t codes_stride, const float *scales, void *x,
+                             int64_t x_stride, int64_t M, int64_t C, int dtype, void *stream);
+
+/* Root-mean-square norm of M rows of C values:
+ *     h = x + residual, rounded to dtype (h = x where residual is null)
+ *     rstd = 1/sqrt(sum(h^2)/C + eps)
+ *     y = gamma * (h*rstd)
+ * or y in 8 bits, of the row t = gamma*h (rounded to fp32), its scale times rstd:
+ * either y, or codes and scales; the others null.  h and residual: both or
+ * neither.  gamma may be null (ones); rstd_out: fp32 [M] or null.  The sum of
+ * squares is fp32: values above 1e18 in magnitude, or below 1e-18 with an eps
+ * below their square, lie outside its range, and in 8 bits so do rows whose
+ * product with gamma leaves fp32's. */
+gn_status gn_rms_norm_rows(const void *x, int64_t x_stride, const void *residual,
+                           int64_t residual_stride, const void *gamma, void *h, int64_t h_stride,
+                           void *y, int64_t y_stride, void *codes, int64_t codes_stride,
+                           float *scales, float *rstd_out, int64_t M, int64_t C, float eps,
+                           int dtype, void *stream);
+
+/* Its backward pass, with rstd as gn_rms_norm_rows wrote it:
+ *     n = h*rstd, g = dy*gamma
+ *     dx = rstd*(g - n*sum(g*n)/C) + dh
+ *     dgamma[c] = sum over rows of dy*n
+ * x holds h (the norm's input, after the residual's addition), or codes and
+ * scales its 8-bit checkpoint (gn_checkpoint_rows), the other null.  dh, the
+ * gradient that reaches h past the norm, and dgamma may be null.  x and the
+ * residual of the forward pass have the same gradient, dx. */
+gn_status gn_rms_norm_rows_backward_workspace(int64_t M, int64_t C, int dtype,
+                                              int64_t *bytes_out);
+gn_status gn_rms_norm_rows_backward(const void *dy, int64_t dy_stride, const void *x,
+                                    int64_t x_stride, const void *codes, const void *scales,
+                                    const float *rstd, const void *gamma, const void *dh,
+                                    int64_t dh_stride, void *dx, int64_t dx_stride, void *dgamma,
+                                    int64_t M, int64_t C, int dtype, void *workspace,
+                                    int64_t workspace_bytes, void *stream);
+
+/* Matrix product of rows in 8 bits with weights in 8 bits, a scale for each row
+ * and for each output channel:
+ *     z[m][n] = (sum_k a[m][k]*w[n][k]) * a_scales[m] * w_scales[n]
+ *               + bias[n] + residual[m][n]
+ * a: int8, row m at m * a_stride (any alignment; up to 15 bytes behind a row,
+ * never across a 16-byte boundary, may be read); packed: the weights w [N][K] as
+ * gn_int8_pack_weights lays them out, w_scales [N]; bias: N values of the
+ * GN_AFFINE_* type of dtype, or null; residual and z: dtype, or residual null.
+ * The sums are int32 and exact; scales, bias and residual are applied in fp32
+ * and z is rounded once.  Codes may be any int8 value.  z == residual with the
+ * same stride is allowed.  Supported: K <= GN_INT8_MAX_K, N <= GN_INT8_MAX_N,
+ * M <= GN_INT8_MAX_M, else GN_UNSUPPORTED; packed 16-byte aligned, workspace too.
+ * gn_int8_matmul_workspace: aligned is 1 when a and (where M > 1) a_stride are
+ * multiples of 16, else 0. */
+#define GN_INT8_MAX_K 65536
+#define GN_INT8_MAX_N (1 << 20)
+#define GN_INT8_MAX_M (1 << 20)
+gn_status gn_int8_packed_bytes(int64_t N, int64_t K, int64_t *bytes_out);
+gn_status gn_int8_pack_weights(const void *codes, int64_t codes_stride, void *packed, int64_t N,
+                               int64_t K, void *stream);
+gn_status gn_int8_matmul_workspace(int64_t M, int64_t N, int64_t K, int aligned,
+                                   int64_t *bytes_out);
+gn_status gn_int8_matmul(const void *a, int64_t a_stride, const float *a_scales, const void *packed,
+                         const float *w_scales, const void *bias, const void *residual,
+                         int64_t residual_stride, void *z, int64_t z_stride, int64_t M, int64_t N,
+                         int64_t K, int dtype, void *workspace, int64_t workspace_bytes,
+                         void *stream);
+
 /* The GroupNorm(+SiLU) fused into the neighbouring 3x3 convolution of the
  * decoder's ResnetBlock2D (Modifications section 2: "ResnetBlock2D
  * norm1/norm2 + SiLU chains" around Conv2d(3x3, p1)):
