@@ -145,7 +145,7 @@ lib.gn_rms_norm_rows_backward.argtypes = [_vp, _i64, _vp, _i64, _vp, _vp, _vp, _
                                           _i64, _vp, _i64, _i64, _int, _vp, _i64, _vp]
 lib.gn_int8_packed_bytes.argtypes = [_i64, _i64, _i64p]
 lib.gn_int8_pack_weights.argtypes = [_vp, _i64, _vp, _i64, _i64, _vp]
-lib.gn_int8_matmul_workspace.argtypes = [_i64, _i64, _i64, _int, _i64p]
+lib.gn_int8_matmul_workspace.argtypes = [_i64, _i64, _i64, _i64p]
 lib.gn_int8_matmul.argtypes = [_vp, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _vp, _i64, _i64, _i64,
                                _i64, _int, _vp, _i64, _vp]
 lib.gn_plan_rows_dtype.argtypes = [_i64, _i64, _i64, _i64, _int, _i64p]
@@ -824,8 +824,7 @@ class Rows8:
     """Rows in 8 bits with a scale each (the format in gnsilu.h): ``codes``
     int8 (..., C), its rows evenly spaced, ``scales`` fp32 (...), contiguous,
     and the ``dtype`` of the rows that they stand for.  The library's own rows
-    start 16 bytes apart or a multiple of that, which is what ``int8_matmul``
-    reads without a copy."""
+    are a multiple of 16 bytes apart, which ``int8_matmul`` reads fastest."""
 
     def __init__(self, codes, scales, dtype):
         torch = _torch()
@@ -1116,8 +1115,7 @@ def int8_matmul(x, weight, bias=None, *, residual=None, dtype=None, out=None):
         if weight is None:
             return None
     step = _row_stride(codes)
-    aligned = 1 if (M == 1 or step % 16 == 0) and codes.data_ptr() % 16 == 0 else 0
-    size = _workspace_bytes("gn_int8_matmul_workspace", M, N, K, aligned)
+    size = _workspace_bytes("gn_int8_matmul_workspace", M, N, K)
     if size is None:
         return None
     ws = torch.empty(size, dtype=torch.uint8, device=codes.device) if size else None

@@ -43,6 +43,9 @@ struct MatmulArgs {
     int kb;               // blocks of 64 input channels, even
     int nb;               // blocks of 16 output channels
     int bias_type;
+    int mt, nt;           // tiles of rows and of channels
+    int split;            // parts of K, each a workgroup's
+    i32x4 *part;          // [split][tiles][...] sums of a part, where split > 1
 };
 
 constexpr int kKBlock = 64, kNBlock = 16, kFragment = 1024;
@@ -67,29 +70,6 @@ __global__ __launch_bounds__(256) void gn_int8_pack(const int8_t *w, int64_t str
     }
     u32x4 o = {v[0], v[1], v[2], v[3]};
     reinterpret_cast<u32x4 *>(packed)[i] = o;
-}
-
-// Rows off 16-byte boundaries, copied to rows on them.
-__global__ __launch_bounds__(256) void gn_int8_align(const int8_t *a, int64_t stride, int8_t *to,
-                                                     int64_t to_stride, int K, int64_t pieces) {
-    const int64_t i = int64_t{blockIdx.x} * 256 + threadIdx.x;
-    if (i >= pieces) return;
-    const int64_t per = to_stride / 16, m = i / per;
-    const int k = static_cast<int>(i % per) * 16;
-    const int8_t *p = a + m * stride + k;
-    u32x4 v;
-    if (k + 16 <= K) {
-        typedef u32x4 u32x4_a1 __attribute__((aligned(1)));
-        v = *reinterpret_cast<const u32x4_a1 *>(p);
-    } else {
-        uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-            if (k + j < K)
-                w[j >> 2] |= static_cast<uint32_t>(static_cast<uint8_t>(p[j])) << (8 * (j & 3));
-        v = u32x4{w[0], w[1], w[2], w[3]};
-    }
-    *reinterpret_cast<u32x4 *>(to + m * to_stride + k) = v;
 }
 
 // ---- the end of a product ----------------------------------------------------------
@@ -145,6 +125,18 @@ __device__ __forceinline__ void finish4(const MatmulArgs &a, int64_t m, int n, c
     }
 }
 
+// 16 bytes of a row from k on, zero behind K.  last: the block may reach behind K.
+typedef u32x4 u32x4_a1 __attribute__((aligned(1)));
+__device__ __forceinline__ u32x4 load16(const int8_t *row, int k, int K, bool last) {
+    if (!last || k + 16 <= K) return *reinterpret_cast<const u32x4_a1 *>(row + k);
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < 15; ++j)
+        if (k + j < K)
+            w[j >> 2] |= static_cast<uint32_t>(static_cast<uint8_t>(row[k + j])) << (8 * (j & 3));
+    return u32x4{w[0], w[1], w[2], w[3]};
+}
+
 // ---- few rows ------------------------------------------------------------------------
 // A workgroup takes 16*MT rows and 16*NT channels; its waves take the blocks of K
 // in turn and join their sums through LDS.
@@ -175,11 +167,10 @@ __global__ __launch_bounds__(WAVES * 64) void gn_int8_rows(MatmulArgs a) {
         for (int u = 0; u < kUnroll; ++u) {
             const int kb = k0 + u * WAVES;
             if (kb >= a.kb) break;
-            const int k = kb * kKBlock + kg;
-            // behind K the weights are zero: any byte of the row will do
-            const int at = k < a.K ? k : 0;
+            const bool last = (kb + 1) * kKBlock > a.K;
 #pragma unroll
-            for (int i = 0; i < MT; ++i) fa[u][i] = *reinterpret_cast<const i32x4 *>(ap[i] + at);
+            for (int i = 0; i < MT; ++i)
+                fa[u][i] = __builtin_bit_cast(i32x4, load16(ap[i], kb * kKBlock + kg, a.K, last));
 #pragma unroll
             for (int j = 0; j < NT; ++j)
                 fb[u][j] = *reinterpret_cast<const i32x4 *>(bp[j] + int64_t{kb} * kFragment);
@@ -209,7 +200,221 @@ __global__ __launch_bounds__(WAVES * 64) void gn_int8_rows(MatmulArgs a) {
     }
 }
 
+// ---- tiles -----------------------------------------------------------------------
+// Eight neighbouring sums of row m from channel n on, scaled and stored.
+template <class D>
+__device__ __forceinline__ void finish8(const MatmulArgs &a, int64_t m, int n, const i32x4 &lo,
+                                        const i32x4 &hi) {
+    using T = typename D::storage;
+    if constexpr (sizeof(T) == 2) {
+        if (m >= a.M || n >= a.N) return;
+        if (n + 8 <= a.N) {
+            const float sa = a.sa[m];
+            float sb[8], b[8], o[8];
+            load_affine<8>(a.sb, Affine::kF32, n, 1.0f, sb);
+            load_affine<8>(a.bias, a.bias_type, n, 0.0f, b);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                o[j] = fmaf(static_cast<float>(j < 4 ? lo[j & 3] : hi[j & 3]) * sa, sb[j], b[j]);
+            if (a.res != nullptr) {
+                Piece<D, 8> r;
+                r.template load<false>(static_cast<const T *>(a.res) + m * a.res_stride + n);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) o[j] += r.get(j);
+            }
+            Piece<D, 8>::template store<false>(static_cast<T *>(a.z) + m * a.z_stride + n, o);
+            return;
+        }
+    }
+    finish4<D>(a, m, n, lo);
+    finish4<D>(a, m, n + 4, hi);
+}
+
+// A 32 x 32 product leaves 4 neighbouring sums of channels 8g + 4*(lane / 32) in
+// each lane, of row lane % 32.  Swapped between the halves of the wave, two g's
+// become 8 neighbours: channels 16*pair + 8*(lane / 32) and up.
+__device__ __forceinline__ void join_halves(i32x4 &g0, i32x4 &g1) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const auto s = __builtin_amdgcn_permlane32_swap(static_cast<uint32_t>(g0[r]),
+                                                        static_cast<uint32_t>(g1[r]), false, false);
+        g0[r] = static_cast<int>(s[0]);
+        g1[r] = static_cast<int>(s[1]);
+    }
+}
+
+// The tile of a workgroup: consecutive workgroups go to the eight XCDs in turn,
+// each of which takes a run of tiles, in strips of kStrip rows of tiles, so
+// that the tiles it works on at one time share rows and weights in its L2.
+constexpr int kStrip = 4;
+__device__ __forceinline__ void tile_of(int b, int tiles, int mt, int nt, int *tm, int *tn) {
+    const int xcd = b & 7, per = tiles >> 3, rest = tiles & 7;
+    const int t = xcd * per + (xcd < rest ? xcd : rest) + (b >> 3);
+    const int strip = t / (kStrip * nt);
+    const int rows = mt - strip * kStrip < kStrip ? mt - strip * kStrip : kStrip;
+    const int in = t - strip * kStrip * nt;
+    *tm = strip * kStrip + in % rows;
+    *tn = in / rows;
+}
+
+// A workgroup of WM x WN waves takes BM = 32*TM*WM rows and BN = 32*TN*WN
+// channels, a wave 32*TM by 32*TN of them, as products of 32 x 32 x 32.  Rows go
+// through LDS, 128 input channels at a time: 16-byte pieces, of row r at place
+// piece ^ (r / 2 % 8) of its 128 bytes, so that the 16 lanes that read one piece
+// of 16 rows find them on different banks.  Weights come straight from memory,
+// in the order in which the lanes hold them.
+template <class D, int WM, int WN, int TM, int TN>
+__global__ __launch_bounds__(WM *WN * 64) void gn_int8_tiles(MatmulArgs a) {
+    constexpr int kThreads = WM * WN * 64, BM = 32 * TM * WM, BN = 32 * TN * WN;
+    constexpr int kStage = BM * 8 / kThreads;  // 16-byte pieces that a lane copies
+    constexpr int kStep = kThreads / 8;        // rows from one of them to the next
+    static_assert(kStep % 16 == 0, "a lane's pieces have one place");
+    __shared__ u32x4 rows[2][BM * 8];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave / WN, wn = wave % WN;
+    const int tiles = a.mt * a.nt;
+    int tm, tn;
+    tile_of(blockIdx.x % tiles, tiles, a.mt, a.nt, &tm, &tn);
+    const int part = blockIdx.x / tiles;
+    const int64_t m0 = int64_t{tm} * BM;
+    const int n0 = tn * BN;
+    // this part's steps of 128 input channels
+    const int all = a.kb / 2, it0 = static_cast<int>(int64_t{all} * part / a.split),
+              it1 = static_cast<int>(int64_t{all} * (part + 1) / a.split);
+
+    const int srow = tid >> 3;
+    const int piece = (tid & 7) ^ (srow >> 1 & 7);
+    const int8_t *ap[kStage];
+#pragma unroll
+    for (int i = 0; i < kStage; ++i) {
+        const int64_t m = m0 + srow + i * kStep;
+        ap[i] = a.a + (m < a.M ? m : a.M - 1) * a.a_stride;
+    }
+    const int8_t *bp[TN];
+#pragma unroll
+    for (int j = 0; j < TN; ++j) {
+        const int nb = n0 / kNBlock + (wn * TN + j) * 2 + (lane >> 4 & 1);
+        bp[j] = a.b + (int64_t{nb < a.nb ? nb : a.nb - 1} * a.kb + it0 * 2) * kFragment +
+                (lane >> 5) * 256 + (lane & 15) * 16;
+    }
+    u32x4 sa[kStage];
+    i32x4 fb[4][TN];
+    auto load_rows = [&](int it) {
+        const int k = it * 128 + piece * 16;
+#pragma unroll
+        for (int i = 0; i < kStage; ++i) sa[i] = load16(ap[i], k, a.K, it + 1 == all);
+    };
+    auto load_weights = [&](int ks) {
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+            fb[ks][j] = *reinterpret_cast<const i32x4 *>(bp[j] + ks * 512);
+    };
+    auto store_rows = [&](int buf) {
+#pragma unroll
+        for (int i = 0; i < kStage; ++i) rows[buf][tid + i * kThreads] = sa[i];
+    };
+    // a lane's piece of row r (of the wave's) at products' step ks
+    const int r0 = wm * TM * 32 + (lane & 31);
+    auto frag = [&](int buf, int t, int ks) {
+        const int r = r0 + t * 32;
+        return *reinterpret_cast<const i32x4 *>(
+            &rows[buf][r * 8 + ((ks * 2 + (lane >> 5)) ^ (r >> 1 & 7))]);
+    };
+    typedef int i32x16 __attribute__((ext_vector_type(16)));
+    i32x16 acc[TM][TN];
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j) acc[i][j] = i32x16{};
+    load_rows(it0);
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks) load_weights(ks);
+    store_rows(0);
+    if (it0 + 1 < it1) load_rows(it0 + 1);
+    for (int it = it0; it < it1; ++it) {
+        const int buf = (it - it0) & 1;
+        __syncthreads();
+        if (it + 1 < it1) {
+            store_rows(buf ^ 1);
+#pragma unroll
+            for (int j = 0; j < TN; ++j) bp[j] += 2 * kFragment;
+        }
+        if (it + 2 < it1) load_rows(it + 2);
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+            i32x4 fa[TM];
+#pragma unroll
+            for (int i = 0; i < TM; ++i) fa[i] = frag(buf, i, ks);
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+#pragma unroll
+                for (int j = 0; j < TN; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[ks][j], fa[i], acc[i][j],
+                                                                       0, 0, 0);
+            if (it + 1 < it1) load_weights(ks);
+        }
+    }
+    if (a.split > 1) {
+        i32x4 *to = a.part + (int64_t{blockIdx.x} * (kThreads / 64) + wave) * (TM * TN * 4 * 64) + lane;
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+#pragma unroll
+                for (int g = 0; g < 4; ++g)
+                    to[((i * TN + j) * 4 + g) * 64] =
+                        i32x4{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2],
+                              acc[i][j][4 * g + 3]};
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+        const int64_t m = m0 + (wm * TM + i) * 32 + (lane & 31);
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                i32x4 g[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) g[h][r] = acc[i][j][8 * p + 4 * h + r];
+                join_halves(g[0], g[1]);
+                finish8<D>(a, m, n0 + (wn * TN + j) * 32 + p * 16 + (lane >> 5) * 8, g[0], g[1]);
+            }
+    }
+}
+
+// The parts of K joined: one wave's lanes as they hold a product's sums.
+template <class D, int WM, int WN, int TM, int TN>
+__global__ __launch_bounds__(256) void gn_int8_join(MatmulArgs a) {
+    constexpr int kWaves = WM * WN, kEach = TM * TN * 2;  // pairs of groups in a wave
+    const int lane = threadIdx.x & 63;
+    const int tiles = a.mt * a.nt;
+    const int64_t u = int64_t{blockIdx.x} * 4 + (threadIdx.x >> 6);
+    if (u >= int64_t{tiles} * kWaves * kEach) return;
+    const int b = static_cast<int>(u / (kWaves * kEach)), in = static_cast<int>(u % (kWaves * kEach));
+    const int wave = in / kEach, pair = in % kEach;
+    const i32x4 *from = a.part + u * 128 + lane;
+    const int64_t next = int64_t{tiles} * kWaves * kEach * 128;
+    i32x4 g0 = {}, g1 = {};
+    for (int s = 0; s < a.split; ++s) {
+        g0 += from[s * next];
+        g1 += from[s * next + 64];
+    }
+    join_halves(g0, g1);
+    int tm, tn;
+    tile_of(b, tiles, a.mt, a.nt, &tm, &tn);
+    const int i = pair / 2 / TN, j = pair / 2 % TN;
+    finish8<D>(a, int64_t{tm} * (32 * TM * WM) + (wave / WN * TM + i) * 32 + (lane & 31),
+               tn * (32 * TN * WN) + (wave % WN * TN + j) * 32 + pair % 2 * 16 + (lane >> 5) * 8, g0,
+               g1);
+}
+
 // ---- host -----------------------------------------------------------------------
+template <int V> using IC = std::integral_constant<int, V>;
+
 template <class F> void by_type(int dtype, F &&f) {
     switch (x_dtype(dtype)) {
         case GN_DTYPE_F16: f(Fp16{}); break;
@@ -235,10 +440,27 @@ gn_status check_nk(int64_t N, int64_t K) {
     return GN_OK;
 }
 
-size_t align_workspace(int64_t M, int64_t K) { return static_cast<size_t>(M * ceil_div(K, 16) * 16); }
+// Which kernel takes a product, and in what tiles.
+struct MatmulPlan {
+    int kind;  // 0: few rows; 1: tiles of 128 x 128; 2: of 256 x 256
+    int mt, nt, split;
+    size_t workspace;
+};
 
-bool rows_aligned(const void *a, int64_t stride, int64_t M) {
-    return !misaligned(a, 16) && (stride % 16 == 0 || M == 1);
+MatmulPlan matmul_plan(int64_t M, int64_t N, int64_t K) {
+    MatmulPlan p{};
+    p.split = 1;
+    if (M <= 64) return p;
+    const int64_t big = ceil_div(M, 256) * ceil_div(N, 256);
+    p.kind = big >= 192 ? 2 : 1;
+    const int64_t side = p.kind == 2 ? 256 : 128;
+    p.mt = static_cast<int>(ceil_div(M, side));
+    p.nt = static_cast<int>(ceil_div(N, side));
+    const int64_t tiles = int64_t{p.mt} * p.nt, steps = k_blocks(K) / 2;
+    if (p.kind == 1)
+        while (tiles * p.split * 2 <= 512 && steps / (p.split * 2) >= 4) p.split *= 2;
+    if (p.split > 1) p.workspace = static_cast<size_t>(tiles * p.split * side * side * 4);
+    return p;
 }
 
 }  // namespace
@@ -274,13 +496,12 @@ gn_status gn_int8_pack_weights(const void *codes, int64_t codes_stride, void *pa
     return finish_launch();
 }
 
-gn_status gn_int8_matmul_workspace(int64_t M, int64_t N, int64_t K, int aligned,
-                                   int64_t *bytes_out) {
-    if (bytes_out == nullptr || M < 0 || (aligned != 0 && aligned != 1)) return GN_INVALID_ARGUMENT;
+gn_status gn_int8_matmul_workspace(int64_t M, int64_t N, int64_t K, int64_t *bytes_out) {
+    if (bytes_out == nullptr || M < 0) return GN_INVALID_ARGUMENT;
     const gn_status st = check_nk(N, K);
     if (st != GN_OK) return st;
     if (M > GN_INT8_MAX_M) return GN_UNSUPPORTED;
-    *bytes_out = aligned ? 0 : static_cast<int64_t>(align_workspace(M, K));
+    *bytes_out = static_cast<int64_t>(matmul_plan(M, N, K).workspace);
     return GN_OK;
 }
 
@@ -307,8 +528,8 @@ gn_status gn_int8_matmul(const void *a, int64_t a_stride, const float *a_scales,
         misaligned(residual, es) || misaligned(z, es) || misaligned(workspace, 16))
         return GN_UNSUPPORTED;
     if (M == 0) return GN_OK;
-    const bool aligned = rows_aligned(a, a_stride, M);
-    const size_t need = aligned ? 0 : align_workspace(M, K);
+    const MatmulPlan plan = matmul_plan(M, N, K);
+    const size_t need = plan.workspace;
     if (need > 0 && workspace == nullptr) return GN_INVALID_ARGUMENT;
     if (need > 0 && (workspace_bytes < 0 || static_cast<size_t>(workspace_bytes) < need))
         return GN_SCRATCH_TOO_SMALL;
@@ -335,25 +556,37 @@ gn_status gn_int8_matmul(const void *a, int64_t a_stride, const float *a_scales,
     p.kb = static_cast<int>(k_blocks(K));
     p.nb = static_cast<int>(n_blocks(N));
     p.bias_type = affine_type(dtype);
-    if (!aligned) {
-        p.a_stride = ceil_div(K, 16) * 16;
-        const int64_t pieces = M * (p.a_stride / 16);
-        gn_int8_align<<<static_cast<unsigned>(ceil_div(pieces, 256)), 256, 0, c.stream>>>(
-            p.a, a_stride, static_cast<int8_t *>(workspace), p.a_stride, p.K, pieces);
-        p.a = static_cast<const int8_t *>(workspace);
-    }
+    p.mt = plan.mt;
+    p.nt = plan.nt;
+    p.split = plan.split;
+    p.part = static_cast<i32x4 *>(workspace);
     by_type(dtype, [&](auto d) {
         using D = decltype(d);
-        auto go = [&](auto mt, auto nt) {
+        auto rows = [&](auto mt, auto nt) {
             constexpr int MT = decltype(mt)::value, NT = decltype(nt)::value, WAVES = 8;
             const dim3 grid(static_cast<unsigned>(ceil_div(p.nb, NT)),
                             static_cast<unsigned>(ceil_div(M, 16 * MT)));
             gn_int8_rows<D, MT, NT, WAVES><<<grid, WAVES * 64, 0, c.stream>>>(p);
         };
-        if (M <= 16)
-            go(std::integral_constant<int, 1>{}, std::integral_constant<int, 1>{});
+        auto tiles = [&](auto wm, auto wn, auto tm, auto tn) {
+            constexpr int WM = decltype(wm)::value, WN = decltype(wn)::value;
+            constexpr int TM = decltype(tm)::value, TN = decltype(tn)::value;
+            const unsigned n = static_cast<unsigned>(p.mt) * static_cast<unsigned>(p.nt);
+            gn_int8_tiles<D, WM, WN, TM, TN>
+                <<<n * static_cast<unsigned>(p.split), WM * WN * 64, 0, c.stream>>>(p);
+            if (p.split > 1)
+                gn_int8_join<D, WM, WN, TM, TN>
+                    <<<static_cast<unsigned>(ceil_div(int64_t{n} * WM * WN * TM * TN * 2, 4)), 256,
+                       0, c.stream>>>(p);
+        };
+        if (plan.kind == 2)
+            tiles(IC<2>{}, IC<4>{}, IC<4>{}, IC<2>{});
+        else if (plan.kind == 1)
+            tiles(IC<2>{}, IC<2>{}, IC<2>{}, IC<2>{});
+        else if (M <= 16)
+            rows(IC<1>{}, IC<1>{});
         else
-            go(std::integral_constant<int, 4>{}, std::integral_constant<int, 2>{});
+            rows(IC<4>{}, IC<2>{});
     });
     return finish_launch();
 }

@@ -503,24 +503,21 @@ gn_status gn_rms_norm_rows_backward(const void *dy, int64_t dy_stride, const voi
  * and for each output channel:
  *     z[m][n] = (sum_k a[m][k]*w[n][k]) * a_scales[m] * w_scales[n]
  *               + bias[n] + residual[m][n]
- * a: int8, row m at m * a_stride (any alignment; up to 15 bytes behind a row,
- * never across a 16-byte boundary, may be read); packed: the weights w [N][K] as
+ * a: int8, row m at m * a_stride (any alignment); packed: the weights w [N][K] as
  * gn_int8_pack_weights lays them out, w_scales [N]; bias: N values of the
  * GN_AFFINE_* type of dtype, or null; residual and z: dtype, or residual null.
  * The sums are int32 and exact; scales, bias and residual are applied in fp32
  * and z is rounded once.  Codes may be any int8 value.  z == residual with the
  * same stride is allowed.  Supported: K <= GN_INT8_MAX_K, N <= GN_INT8_MAX_N,
- * M <= GN_INT8_MAX_M, else GN_UNSUPPORTED; packed 16-byte aligned, workspace too.
- * gn_int8_matmul_workspace: aligned is 1 when a and (where M > 1) a_stride are
- * multiples of 16, else 0. */
+ * M <= GN_INT8_MAX_M, else GN_UNSUPPORTED; packed 16-byte aligned, workspace
+ * too. */
 #define GN_INT8_MAX_K 65536
 #define GN_INT8_MAX_N (1 << 20)
 #define GN_INT8_MAX_M (1 << 20)
 gn_status gn_int8_packed_bytes(int64_t N, int64_t K, int64_t *bytes_out);
 gn_status gn_int8_pack_weights(const void *codes, int64_t codes_stride, void *packed, int64_t N,
                                int64_t K, void *stream);
-gn_status gn_int8_matmul_workspace(int64_t M, int64_t N, int64_t K, int aligned,
-                                   int64_t *bytes_out);
+gn_status gn_int8_matmul_workspace(int64_t M, int64_t N, int64_t K, int64_t *bytes_out);
 gn_status gn_int8_matmul(const void *a, int64_t a_stride, const float *a_scales, const void *packed,
                          const float *w_scales, const void *bias, const void *residual,
                          int64_t residual_stride, void *z, int64_t z_stride, int64_t M, int64_t N,

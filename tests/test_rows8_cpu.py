@@ -78,7 +78,7 @@ def product(a=P[0], as_=64, sa=P[1], w=P[2], sw=P[3], bias=P[4], res=P[5], rs=32
     (product, dict(sw=None)), (product, dict(z=None)), (product, dict(M=-1)),
     (product, dict(N=0)), (product, dict(K=-1)), (product, dict(dtype=3)),
     (product, dict(zs=31)), (product, dict(as_=-16)), (product, dict(rs=-1)),
-    (product, dict(as_=BIG)), (product, dict(as_=60, ws=None)), (product, dict(a=ODD, ws=None)),
+    (product, dict(as_=BIG)), (product, dict(M=300, K=16384, as_=16384, ws=None)),
 ])
 def test_invalid(fn, kw):
     assert fn(**kw) == GnStatus.INVALID_ARGUMENT
@@ -139,14 +139,17 @@ def test_workspace_sizes():
     assert pb(4, 4, None) == GnStatus.INVALID_ARGUMENT
 
     mw = gn.gn_int8_matmul_workspace
-    st, n = size_of(mw, 9, 32, 65, 0)
-    assert st == GnStatus.OK and n >= 9 * 65
-    assert product(M=9, K=65, as_=65, size=n - 1) == GnStatus.SCRATCH_TOO_SMALL
-    assert product(M=9, K=65, as_=65, size=-1) == GnStatus.SCRATCH_TOO_SMALL
-    assert size_of(mw, 9, 32, 64, 2)[0] == GnStatus.INVALID_ARGUMENT
-    assert size_of(mw, -1, 32, 64, 1)[0] == GnStatus.INVALID_ARGUMENT
-    assert size_of(mw, 1, 0, 64, 1)[0] == GnStatus.INVALID_ARGUMENT
-    assert mw(1, 32, 64, 1, None) == GnStatus.INVALID_ARGUMENT
+    for M in (1, 16, 64):               # few rows need none
+        assert size_of(mw, M, 4096, 4096) == (GnStatus.OK, 0)
+    st, n = size_of(mw, 300, 32, 16384)     # few tiles: K in parts
+    assert st == GnStatus.OK and n >= 2 * 4 * 300 * 32
+    assert product(M=300, K=16384, as_=16384, size=n - 1) == GnStatus.SCRATCH_TOO_SMALL
+    assert product(M=300, K=16384, as_=16384, size=-1) == GnStatus.SCRATCH_TOO_SMALL
+    assert size_of(mw, -1, 32, 64)[0] == GnStatus.INVALID_ARGUMENT
+    assert size_of(mw, 1, 0, 64)[0] == GnStatus.INVALID_ARGUMENT
+    assert size_of(mw, 1, 32, 65537)[0] == GnStatus.UNSUPPORTED
+    assert size_of(mw, (1 << 20) + 1, 32, 64)[0] == GnStatus.UNSUPPORTED
+    assert mw(1, 32, 64, None) == GnStatus.INVALID_ARGUMENT
 
 
 # ---- the binding ---------------------------------------------------------------
