@@ -269,7 +269,7 @@ __global__ __launch_bounds__(WM *WN * 64) void gn_int8_tiles(MatmulArgs a) {
     constexpr int kStage = BM * 8 / kThreads;  // 16-byte pieces that a lane copies
     constexpr int kStep = kThreads / 8;        // rows from one of them to the next
     static_assert(kStep % 16 == 0, "a lane's pieces have one place");
-    __shared__ u32x4 rows[2][BM * 8];
+    __shared__ u32x4 rows[3][BM * 8];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / WN, wn = wave % WN;
@@ -300,10 +300,12 @@ __global__ __launch_bounds__(WM *WN * 64) void gn_int8_tiles(MatmulArgs a) {
     }
     u32x4 sa[kStage];
     i32x4 fb[4][TN];
-    auto load_rows = [&](int it) {
+    // FULL: a step that lies wholly inside K, as all but the last are
+    auto load_rows = [&](auto full, int it) {
         const int k = it * 128 + piece * 16;
 #pragma unroll
-        for (int i = 0; i < kStage; ++i) sa[i] = load16(ap[i], k, a.K, it + 1 == all);
+        for (int i = 0; i < kStage; ++i)
+            sa[i] = load16(ap[i], k, a.K, !decltype(full)::value && it + 1 == all);
     };
     auto load_weights = [&](int ks) {
 #pragma unroll
@@ -327,34 +329,62 @@ __global__ __launch_bounds__(WM *WN * 64) void gn_int8_tiles(MatmulArgs a) {
     for (int i = 0; i < TM; ++i)
 #pragma unroll
         for (int j = 0; j < TN; ++j) acc[i][j] = i32x16{};
-    load_rows(it0);
-#pragma unroll
-    for (int ks = 0; ks < 4; ++ks) load_weights(ks);
-    store_rows(0);
-    if (it0 + 1 < it1) load_rows(it0 + 1);
-    for (int it = it0; it < it1; ++it) {
-        const int buf = (it - it0) & 1;
-        __syncthreads();
-        if (it + 1 < it1) {
-            store_rows(buf ^ 1);
+    // One step.  The next one's rows go from registers to LDS and those of the one
+    // after it start on their way (`full`: there are both, wholly inside K); each
+    // product's operands are read while the product before it runs, and the next
+    // step's weights replace each product's as they are used.  With three buffers
+    // one barrier is enough, in the middle, where no wave waits for it long: what
+    // is written here was last read two steps ago.  The compiler would move the
+    // loads behind the products, next to their use: the scheduling barriers keep
+    // them where they are.
+    i32x4 fa[2][TM];
+    int cur = 0;
+    auto step = [&](auto full, int it) {
+        constexpr bool kFull = decltype(full)::value != 0;
+        const int next = cur == 2 ? 0 : cur + 1;
+        if (kFull || it + 1 < it1) {
+            store_rows(next);
 #pragma unroll
             for (int j = 0; j < TN; ++j) bp[j] += 2 * kFragment;
         }
-        if (it + 2 < it1) load_rows(it + 2);
+        if (kFull || it + 2 < it1) load_rows(full, it + 2);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) {
-            i32x4 fa[TM];
+            if (ks < 3 || kFull || it + 1 < it1) {
 #pragma unroll
-            for (int i = 0; i < TM; ++i) fa[i] = frag(buf, i, ks);
+                for (int i = 0; i < TM; ++i)
+                    fa[(ks + 1) & 1][i] = ks < 3 ? frag(cur, i, ks + 1) : frag(next, i, 0);
+            }
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int i = 0; i < TM; ++i)
 #pragma unroll
                 for (int j = 0; j < TN; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[ks][j], fa[i], acc[i][j],
-                                                                       0, 0, 0);
-            if (it + 1 < it1) load_weights(ks);
+                    acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[ks][j], fa[ks & 1][i],
+                                                                       acc[i][j], 0, 0, 0);
+            __builtin_amdgcn_sched_barrier(0);
+            if (kFull || it + 1 < it1) load_weights(ks);
+            if (ks == 1) __syncthreads();
+            __builtin_amdgcn_sched_barrier(0);
         }
-    }
+        cur = next;
+    };
+    typedef std::integral_constant<int, 0> Any;
+    typedef std::integral_constant<int, 1> Full;
+    load_rows(Any{}, it0);
+    store_rows(0);
+    // rows before weights, as in a step: a wait for the former is none for the latter
+    if (it0 + 1 < it1) load_rows(Any{}, it0 + 1);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks) load_weights(ks);
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < TM; ++i) fa[0][i] = frag(0, i, 0);
+    int it = it0;
+    for (; it + 3 < it1; ++it) step(Full{}, it);
+    for (; it < it1; ++it) step(Any{}, it);
     if (a.split > 1) {
         i32x4 *to = a.part + (int64_t{blockIdx.x} * (kThreads / 64) + wave) * (TM * TN * 4 * 64) + lane;
 #pragma unroll
