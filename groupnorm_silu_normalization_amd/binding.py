@@ -145,9 +145,9 @@ lib.gn_rms_norm_rows_backward.argtypes = [_vp, _i64, _vp, _i64, _vp, _vp, _vp, _
                                           _i64, _vp, _i64, _i64, _int, _vp, _i64, _vp]
 lib.gn_int8_packed_bytes.argtypes = [_i64, _i64, _i64p]
 lib.gn_int8_pack_weights.argtypes = [_vp, _i64, _vp, _i64, _i64, _vp]
-lib.gn_int8_matmul_workspace.argtypes = [_i64, _i64, _i64, _i64p]
+lib.gn_int8_matmul_plan.argtypes = [_i64, _i64, _i64, _i64, _i64p]
 lib.gn_int8_matmul.argtypes = [_vp, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _vp, _i64, _i64, _i64,
-                               _i64, _int, _vp, _i64, _vp]
+                               _i64, _int, _vp]
 lib.gn_plan_rows_dtype.argtypes = [_i64, _i64, _i64, _i64, _int, _i64p]
 lib.gn_plan_single_launch.argtypes = [_i64, _i64, _i64, _i64, _int, _i64p]
 for _name in ("gn_silu_nhwc", "gn_silu_rows", "gn_silu_nhwc_strided", "gn_stats_rows",
@@ -162,8 +162,8 @@ for _name in ("gn_silu_nhwc", "gn_silu_rows", "gn_silu_nhwc_strided", "gn_stats_
               "gn_apply_rows_save", "gn_silu_rows_backward_workspace", "gn_silu_rows_backward",
               "gn_quantize_rows", "gn_dequantize_rows", "gn_rms_norm_rows",
               "gn_rms_norm_rows_backward_workspace", "gn_rms_norm_rows_backward",
-              "gn_int8_packed_bytes", "gn_int8_pack_weights", "gn_int8_matmul_workspace",
-              "gn_int8_matmul"):
+              "gn_int8_packed_bytes", "gn_int8_pack_weights", "gn_int8_matmul",
+              "gn_int8_matmul_plan"):
     getattr(lib, _name).restype = _int
 lib.gn_plan_rows.argtypes = [_i64, _i64, _i64, _i64, _i64p]
 lib.gn_plan_rows.restype = _int
@@ -217,8 +217,8 @@ gn_rms_norm_rows_backward_workspace = lib.gn_rms_norm_rows_backward_workspace
 gn_rms_norm_rows_backward = lib.gn_rms_norm_rows_backward
 gn_int8_packed_bytes = lib.gn_int8_packed_bytes
 gn_int8_pack_weights = lib.gn_int8_pack_weights
-gn_int8_matmul_workspace = lib.gn_int8_matmul_workspace
 gn_int8_matmul = lib.gn_int8_matmul
+gn_int8_matmul_plan = lib.gn_int8_matmul_plan
 gn_status_string = lib.gn_status_string
 gn_version = lib.gn_version
 gn_device_info = lib.gn_device_info
@@ -1115,15 +1115,22 @@ def int8_matmul(x, weight, bias=None, *, residual=None, dtype=None, out=None):
         if weight is None:
             return None
     step = _row_stride(codes)
-    size = _workspace_bytes("gn_int8_matmul_workspace", M, N, K)
-    if size is None:
-        return None
-    ws = torch.empty(size, dtype=torch.uint8, device=codes.device) if size else None
     code = _run(
         lib.gn_int8_matmul, codes, _addr(codes), step, _addr(x.scales), _addr(weight.data),
         _addr(weight.scales), _addr(bias), _addr(residual), rstep, _addr(out), zstep, M, N, K,
-        dtype_code(dtype) | _affine_flag(bias, None), _addr(ws), size)
+        dtype_code(dtype) | _affine_flag(bias, None))
     return _result(code, out)
+
+
+INT8_PLAN_FIELDS = ("rows", "channels", "tiles_kernel", "workgroups")
+
+
+def int8_matmul_plan(M, N, K, row_stride=None):
+    """The library's launch shape for int8_matmul (dict), or None if declined."""
+    buf = (_i64 * len(INT8_PLAN_FIELDS))()
+    r = _result(lib.gn_int8_matmul_plan(M, N, K, K if row_stride is None else row_stride, buf),
+                True)
+    return None if r is None else dict(zip(INT8_PLAN_FIELDS, list(buf)))
 
 
 PLAN_FIELDS = ("slots", "tiles", "full", "tpc1", "K1", "tpc2", "K2", "scratch_bytes",

@@ -44,8 +44,6 @@ struct MatmulArgs {
     int nb;               // blocks of 16 output channels
     int bias_type;
     int mt, nt;           // tiles of rows and of channels
-    int split;            // parts of K, each a workgroup's
-    i32x4 *part;          // [split][tiles][...] sums of a part, where split > 1
 };
 
 constexpr int kKBlock = 64, kNBlock = 16, kFragment = 1024;
@@ -125,34 +123,64 @@ __device__ __forceinline__ void finish4(const MatmulArgs &a, int64_t m, int n, c
     }
 }
 
-// 16 bytes of a row from k on, zero behind K.  last: the block may reach behind K.
+// The tile of a workgroup: consecutive workgroups go to the eight XCDs in turn,
+// each of which takes a run of tiles, in strips of kStrip rows of tiles, so
+// that the tiles it works on at one time share rows and weights in its L2.
+constexpr int kStrip = 4;
+__device__ __forceinline__ void tile_of(int b, int tiles, int mt, int nt, int *tm, int *tn) {
+    const int xcd = b & 7, per = tiles >> 3, rest = tiles & 7;
+    const int t = xcd * per + (xcd < rest ? xcd : rest) + (b >> 3);
+    const int strip = t / (kStrip * nt);
+    const int rows = mt - strip * kStrip < kStrip ? mt - strip * kStrip : kStrip;
+    const int in = t - strip * kStrip * nt;
+    *tm = strip * kStrip + in % rows;
+    *tn = in / rows;
+}
+
+// 16 bytes of a row from k on.  What lies behind K is multiplied by packed zeros:
+// any bytes will do that may be read, the next row's or, from `end` on (behind
+// the last row), none.  last: the block may reach behind K.
 typedef u32x4 u32x4_a1 __attribute__((aligned(1)));
-__device__ __forceinline__ u32x4 load16(const int8_t *row, int k, int K, bool last) {
-    if (!last || k + 16 <= K) return *reinterpret_cast<const u32x4_a1 *>(row + k);
-    uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-    for (int j = 0; j < 15; ++j)
-        if (k + j < K)
-            w[j >> 2] |= static_cast<uint32_t>(static_cast<uint8_t>(row[k + j])) << (8 * (j & 3));
-    return u32x4{w[0], w[1], w[2], w[3]};
+__device__ __forceinline__ i32x4 load16(const int8_t *row, int k, int K, const int8_t *end, bool last) {
+    const int8_t *p = row + k;
+    if (!last || (k < K && end - p >= 16))
+        return __builtin_bit_cast(i32x4, *reinterpret_cast<const u32x4_a1 *>(p));
+    uint64_t w[2] = {0, 0};
+#pragma unroll 1
+    for (int j = 0; k + j < K && j < 16; ++j) {
+        const uint64_t v = static_cast<uint64_t>(static_cast<uint8_t>(p[j])) << (8 * (j & 7));
+        if (j < 8)
+            w[0] |= v;
+        else
+            w[1] |= v;
+    }
+    return i32x4{static_cast<int>(w[0]), static_cast<int>(w[0] >> 32), static_cast<int>(w[1]),
+                 static_cast<int>(w[1] >> 32)};
 }
 
 // ---- few rows ------------------------------------------------------------------------
-// A workgroup takes 16*MT rows and 16*NT channels; its waves take the blocks of K
-// in turn and join their sums through LDS.
+// A workgroup takes 16*MT rows and 16*NT channels; its waves take the steps of
+// 128 input channels in turn and join their sums through LDS at the end, so that
+// nothing waits for another wave before.  A wave loads eight rows' 128 bytes an
+// instruction (16 rows' 64 bytes, as products want them, come at a third of the
+// rate) and turns them in a corner of LDS of its own; weights come as products
+// want them.  The next step's loads are on their way while one is multiplied.
 template <class D, int MT, int NT, int WAVES>
 __global__ __launch_bounds__(WAVES * 64) void gn_int8_rows(MatmulArgs a) {
-    constexpr int kTiles = MT * NT, kUnroll = 2;
-    __shared__ i32x4 part[WAVES][kTiles][64];
+    constexpr int kTiles = MT * NT, kOwn = 64 * (kTiles > 2 * MT ? kTiles : 2 * MT);
+    __shared__ i32x4 lds[WAVES][kOwn];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
-    const int64_t m0 = int64_t{blockIdx.y} * (16 * MT);
-    const int nb0 = static_cast<int>(blockIdx.x) * NT;
-    const int kg = (lane >> 4) * 16;
-    const int8_t *ap[MT], *bp[NT];
+    i32x4 *own = lds[wave];
+    int tm, tn;
+    tile_of(blockIdx.x, a.mt * a.nt, a.mt, a.nt, &tm, &tn);
+    const int64_t m0 = int64_t{tm} * (16 * MT);
+    const int nb0 = tn * NT;
+    const int8_t *end = a.a + (a.M - 1) * a.a_stride + a.K;
+    const int8_t *ap[2 * MT], *bp[NT];
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-        const int64_t m = m0 + i * 16 + (lane & 15);
+    for (int i = 0; i < 2 * MT; ++i) {
+        const int64_t m = m0 + i * 8 + (lane >> 3);
         ap[i] = a.a + (m < a.M ? m : a.M - 1) * a.a_stride;
     }
 #pragma unroll
@@ -160,74 +188,141 @@ __global__ __launch_bounds__(WAVES * 64) void gn_int8_rows(MatmulArgs a) {
         const int nb = nb0 + j < a.nb ? nb0 + j : a.nb - 1;
         bp[j] = a.b + int64_t{nb} * a.kb * kFragment + lane * 16;
     }
+    // piece p of row r lies at place p ^ (r / 2 % 8): a lane's row is i*8 + lane/8
+    const int piece[2] = {(lane & 7) ^ (lane >> 4), (lane & 7) ^ (lane >> 4) ^ 4};
+    const int steps = a.kb / 2;
+    i32x4 sa[2 * MT], fb[2][NT];
+    auto load_rows = [&](int it) {
+        const bool last = (it + 1) * 2 * kKBlock > a.K;
+#pragma unroll
+        for (int i = 0; i < 2 * MT; ++i)
+            sa[i] = load16(ap[i], it * 128 + piece[i & 1] * 16, a.K, end, last);
+    };
+    auto load_weights = [&](int it, int u) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+            fb[u][j] = *reinterpret_cast<const i32x4 *>(bp[j] + int64_t{it * 2 + u} * kFragment);
+    };
     i32x4 acc[MT][NT] = {};
-    for (int k0 = wave; k0 < a.kb; k0 += kUnroll * WAVES) {
-        i32x4 fa[kUnroll][MT], fb[kUnroll][NT];
+    int it = wave;
+    if (it < steps) {
+        load_rows(it);
+        load_weights(it, 0);
+        load_weights(it, 1);
+    }
+    for (; it < steps; it += WAVES) {
+        const bool more = it + WAVES < steps;
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const int kb = k0 + u * WAVES;
-            if (kb >= a.kb) break;
-            const bool last = (kb + 1) * kKBlock > a.K;
+        for (int i = 0; i < 2 * MT; ++i) own[i * 64 + lane] = sa[i];
+        // the lanes of one wave: LDS works in order, the compiler is told to
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+        if (more) load_rows(it + WAVES);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int i = 0; i < MT; ++i)
-                fa[u][i] = __builtin_bit_cast(i32x4, load16(ap[i], kb * kKBlock + kg, a.K, last));
+        for (int u = 0; u < 2; ++u) {
+            i32x4 fa[MT];
 #pragma unroll
-            for (int j = 0; j < NT; ++j)
-                fb[u][j] = *reinterpret_cast<const i32x4 *>(bp[j] + int64_t{kb} * kFragment);
-        }
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            if (k0 + u * WAVES >= a.kb) break;
+            for (int i = 0; i < MT; ++i) {
+                const int r = i * 16 + (lane & 15);
+                fa[i] = own[r * 8 + ((u * 4 + (lane >> 4)) ^ (r >> 1 & 7))];
+            }
 #pragma unroll
             for (int i = 0; i < MT; ++i)
 #pragma unroll
                 for (int j = 0; j < NT; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[u][j], fa[u][i], acc[i][j],
-                                                                       0, 0, 0);
+                    acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[u][j], fa[i], acc[i][j], 0,
+                                                                       0, 0);
+            if (more) load_weights(it + WAVES, u);
+            __builtin_amdgcn_sched_barrier(0);
         }
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
     }
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
-        for (int j = 0; j < NT; ++j) part[wave][i * NT + j][lane] = acc[i][j];
+        for (int j = 0; j < NT; ++j) own[(i * NT + j) * 64 + lane] = acc[i][j];
     __syncthreads();
     for (int tile = wave; tile < kTiles; tile += WAVES) {
-        i32x4 s = part[0][tile][lane];
+        i32x4 s = lds[0][tile * 64 + lane];
 #pragma unroll
-        for (int w = 1; w < WAVES; ++w) s += part[w][tile][lane];
+        for (int w = 1; w < WAVES; ++w) s += lds[w][tile * 64 + lane];
         finish4<D>(a, m0 + tile / NT * 16 + (lane & 15),
                    (nb0 + tile % NT) * kNBlock + (lane >> 4) * 4, s);
     }
 }
 
 // ---- tiles -----------------------------------------------------------------------
-// Eight neighbouring sums of row m from channel n on, scaled and stored.
-template <class D>
-__device__ __forceinline__ void finish8(const MatmulArgs &a, int64_t m, int n, const i32x4 &lo,
-                                        const i32x4 &hi) {
-    using T = typename D::storage;
-    if constexpr (sizeof(T) == 2) {
-        if (m >= a.M || n >= a.N) return;
+// Scales and bias of eight neighbouring channels; those behind N count nothing.
+struct Channels8 {
+    float s[8], b[8];
+    __device__ __forceinline__ Channels8(const MatmulArgs &a, int n) {
         if (n + 8 <= a.N) {
-            const float sa = a.sa[m];
-            float sb[8], b[8], o[8];
-            load_affine<8>(a.sb, Affine::kF32, n, 1.0f, sb);
+            load_affine<8>(a.sb, Affine::kF32, n, 1.0f, s);
             load_affine<8>(a.bias, a.bias_type, n, 0.0f, b);
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                o[j] = fmaf(static_cast<float>(j < 4 ? lo[j & 3] : hi[j & 3]) * sa, sb[j], b[j]);
-            if (a.res != nullptr) {
-                Piece<D, 8> r;
-                r.template load<false>(static_cast<const T *>(a.res) + m * a.res_stride + n);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) o[j] += r.get(j);
-            }
-            Piece<D, 8>::template store<false>(static_cast<T *>(a.z) + m * a.z_stride + n, o);
             return;
         }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int c = n + j < a.N ? n + j : a.N - 1;
+            float v[1];
+            load_affine<1>(a.bias, a.bias_type, c, 0.0f, v);
+            s[j] = a.sb[c];
+            b[j] = v[0];
+        }
     }
-    finish4<D>(a, m, n, lo);
-    finish4<D>(a, m, n + 4, hi);
+};
+
+// Eight neighbouring sums of TM rows (32 apart) from channel n on, scaled and
+// stored; the residual's loads all before the first store.
+template <class D, int TM>
+__device__ __forceinline__ void finish8(const MatmulArgs &a, int64_t m0, int n, const float (&sa)[TM],
+                                        const i32x4 (&lo)[TM], const i32x4 (&hi)[TM]) {
+    using T = typename D::storage;
+    if (n >= a.N) return;
+    const Channels8 ch(a, n);
+    T *z = static_cast<T *>(a.z) + m0 * a.z_stride + n;
+    const T *res = static_cast<const T *>(a.res) + m0 * a.res_stride + n;
+    constexpr int W = sizeof(T) == 2 ? 8 : 4;
+    const bool whole = n + 8 <= a.N;
+    Piece<D, W> r[TM][8 / W];
+    if (a.res != nullptr && whole) {
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int k = 0; k < 8 / W; ++k)
+                if (m0 + i * 32 < a.M)
+                    r[i][k].template load<false>(res + i * 32 * a.res_stride + k * W);
+    }
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+        if (m0 + i * 32 >= a.M) break;
+        float o[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            o[j] = fmaf(static_cast<float>(j < 4 ? lo[i][j & 3] : hi[i][j & 3]) * sa[i], ch.s[j],
+                        ch.b[j]);
+        if (whole) {
+#pragma unroll
+            for (int k = 0; k < 8 / W; ++k) {
+                float v[W];
+#pragma unroll
+                for (int j = 0; j < W; ++j)
+                    v[j] = a.res != nullptr ? o[k * W + j] + r[i][k].get(j) : o[k * W + j];
+                Piece<D, W>::template store<false>(z + i * 32 * a.z_stride + k * W, v);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                if (n + j >= a.N) break;
+                if (a.res != nullptr) o[j] += D::to_f32(res[i * 32 * a.res_stride + j]);
+                z[i * 32 * a.z_stride + j] = D::from_f32(o[j]);
+            }
+        }
+    }
 }
 
 // A 32 x 32 product leaves 4 neighbouring sums of channels 8g + 4*(lane / 32) in
@@ -243,85 +338,68 @@ __device__ __forceinline__ void join_halves(i32x4 &g0, i32x4 &g1) {
     }
 }
 
-// The tile of a workgroup: consecutive workgroups go to the eight XCDs in turn,
-// each of which takes a run of tiles, in strips of kStrip rows of tiles, so
-// that the tiles it works on at one time share rows and weights in its L2.
-constexpr int kStrip = 4;
-__device__ __forceinline__ void tile_of(int b, int tiles, int mt, int nt, int *tm, int *tn) {
-    const int xcd = b & 7, per = tiles >> 3, rest = tiles & 7;
-    const int t = xcd * per + (xcd < rest ? xcd : rest) + (b >> 3);
-    const int strip = t / (kStrip * nt);
-    const int rows = mt - strip * kStrip < kStrip ? mt - strip * kStrip : kStrip;
-    const int in = t - strip * kStrip * nt;
-    *tm = strip * kStrip + in % rows;
-    *tn = in / rows;
-}
-
-// A workgroup of WM x WN waves takes BM = 32*TM*WM rows and BN = 32*TN*WN
-// channels, a wave 32*TM by 32*TN of them, as products of 32 x 32 x 32.  Rows go
-// through LDS, 128 input channels at a time: 16-byte pieces, of row r at place
-// piece ^ (r / 2 % 8) of its 128 bytes, so that the 16 lanes that read one piece
-// of 16 rows find them on different banks.  Weights come straight from memory,
-// in the order in which the lanes hold them.
-template <class D, int WM, int WN, int TM, int TN>
-__global__ __launch_bounds__(WM *WN * 64) void gn_int8_tiles(MatmulArgs a) {
-    constexpr int kThreads = WM * WN * 64, BM = 32 * TM * WM, BN = 32 * TN * WN;
+// A workgroup of WN waves takes BM = 32*TM rows and BN = 32*TN*WN channels, a wave
+// all the rows and 32*TN of the channels, as products of 32 x 32 x 32.  Rows go
+// through LDS, 128 input channels at a time: 16-byte pieces, piece p of row r at
+// place p ^ (r / 2 % 8) of its 128 bytes, so that the 16 lanes that read one piece
+// of 16 rows find them on different banks.  Weights come straight from memory, in
+// the order in which the lanes hold them, and as no two waves share channels they
+// are read once: what a CU gets from its L2 (about 40 bytes a clock) bounds these
+// tiles, not the products.
+template <class D, int WN, int TM, int TN, int AHEAD>
+__global__ __launch_bounds__(WN * 64, 2) void gn_int8_tiles(MatmulArgs a) {
+    constexpr int kThreads = WN * 64, BM = 32 * TM, BN = 32 * TN * WN;
     constexpr int kStage = BM * 8 / kThreads;  // 16-byte pieces that a lane copies
     constexpr int kStep = kThreads / 8;        // rows from one of them to the next
     static_assert(kStep % 16 == 0, "a lane's pieces have one place");
-    __shared__ u32x4 rows[3][BM * 8];
+    static_assert(kStage % 2 == 0, "half of them in each half of a step");
+    __shared__ i32x4 rows[3][BM * 8];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wm = wave / WN, wn = wave % WN;
-    const int tiles = a.mt * a.nt;
     int tm, tn;
-    tile_of(blockIdx.x % tiles, tiles, a.mt, a.nt, &tm, &tn);
-    const int part = blockIdx.x / tiles;
+    tile_of(blockIdx.x, a.mt * a.nt, a.mt, a.nt, &tm, &tn);
     const int64_t m0 = int64_t{tm} * BM;
-    const int n0 = tn * BN;
-    // this part's steps of 128 input channels
-    const int all = a.kb / 2, it0 = static_cast<int>(int64_t{all} * part / a.split),
-              it1 = static_cast<int>(int64_t{all} * (part + 1) / a.split);
+    const int n0 = tn * BN + wave * TN * 32;
+    const int steps = a.kb / 2;  // of 128 input channels
 
+    // Addresses: one of the tile's rows and one of its weights, the same for all
+    // lanes, and 32-bit distances from them.
+    const int8_t *arow = a.a + m0 * a.a_stride;
+    const int8_t *end = a.a + (a.M - 1) * a.a_stride + a.K;
     const int srow = tid >> 3;
     const int piece = (tid & 7) ^ (srow >> 1 & 7);
-    const int8_t *ap[kStage];
+    uint32_t aoff[kStage];
 #pragma unroll
     for (int i = 0; i < kStage; ++i) {
-        const int64_t m = m0 + srow + i * kStep;
-        ap[i] = a.a + (m < a.M ? m : a.M - 1) * a.a_stride;
+        const int64_t r = srow + i * kStep;
+        aoff[i] = static_cast<uint32_t>((m0 + r < a.M ? r : a.M - 1 - m0) * a.a_stride);
     }
-    const int8_t *bp[TN];
+    const int nb0 = n0 / kNBlock < a.nb ? n0 / kNBlock : a.nb - 1;
+    const int8_t *brow = a.b + int64_t{nb0} * a.kb * kFragment;
+    uint32_t boff[TN];
 #pragma unroll
     for (int j = 0; j < TN; ++j) {
-        const int nb = n0 / kNBlock + (wn * TN + j) * 2 + (lane >> 4 & 1);
-        bp[j] = a.b + (int64_t{nb < a.nb ? nb : a.nb - 1} * a.kb + it0 * 2) * kFragment +
-                (lane >> 5) * 256 + (lane & 15) * 16;
+        const int nb = j * 2 + (lane >> 4 & 1);
+        boff[j] = static_cast<uint32_t>(nb0 + nb < a.nb ? nb : a.nb - 1 - nb0) *
+                      static_cast<uint32_t>(a.kb * kFragment) +
+                  static_cast<uint32_t>((lane >> 5) * 256 + (lane & 15) * 16);
     }
-    u32x4 sa[kStage];
-    i32x4 fb[4][TN];
+    i32x4 sa[AHEAD][kStage];
+    i32x4 fb[AHEAD][4][TN];
     // FULL: a step that lies wholly inside K, as all but the last are
-    auto load_rows = [&](auto full, int it) {
-        const int k = it * 128 + piece * 16;
-#pragma unroll
-        for (int i = 0; i < kStage; ++i)
-            sa[i] = load16(ap[i], k, a.K, !decltype(full)::value && it + 1 == all);
+    auto load_row = [&](auto full, int q, int i, int it) {
+        sa[q][i] = load16(arow + aoff[i], it * 128 + piece * 16, a.K, end,
+                          !decltype(full)::value && it + 1 == steps);
     };
-    auto load_weights = [&](int ks) {
-#pragma unroll
-        for (int j = 0; j < TN; ++j)
-            fb[ks][j] = *reinterpret_cast<const i32x4 *>(bp[j] + ks * 512);
+    auto load_weight = [&](int q, int ks, int j, int it) {
+        fb[q][ks][j] = *reinterpret_cast<const i32x4 *>(brow + int64_t{it} * (2 * kFragment) +
+                                                        boff[j] + ks * 512);
     };
-    auto store_rows = [&](int buf) {
-#pragma unroll
-        for (int i = 0; i < kStage; ++i) rows[buf][tid + i * kThreads] = sa[i];
-    };
-    // a lane's piece of row r (of the wave's) at products' step ks
-    const int r0 = wm * TM * 32 + (lane & 31);
+    auto store_row = [&](int q, int i, int buf) { rows[buf][tid + i * kThreads] = sa[q][i]; };
+    // a lane's piece of its row among rows 32*t and up, for product step ks
     auto frag = [&](int buf, int t, int ks) {
-        const int r = r0 + t * 32;
-        return *reinterpret_cast<const i32x4 *>(
-            &rows[buf][r * 8 + ((ks * 2 + (lane >> 5)) ^ (r >> 1 & 7))]);
+        const int r = t * 32 + (lane & 31);
+        return rows[buf][r * 8 + ((ks * 2 + (lane >> 5)) ^ (r >> 1 & 7))];
     };
     typedef int i32x16 __attribute__((ext_vector_type(16)));
     i32x16 acc[TM][TN];
@@ -329,42 +407,46 @@ __global__ __launch_bounds__(WM *WN * 64) void gn_int8_tiles(MatmulArgs a) {
     for (int i = 0; i < TM; ++i)
 #pragma unroll
         for (int j = 0; j < TN; ++j) acc[i][j] = i32x16{};
-    // One step.  The next one's rows go from registers to LDS and those of the one
-    // after it start on their way (`full`: there are both, wholly inside K); each
-    // product's operands are read while the product before it runs, and the next
-    // step's weights replace each product's as they are used.  With three buffers
-    // one barrier is enough, in the middle, where no wave waits for it long: what
-    // is written here was last read two steps ago.  The compiler would move the
-    // loads behind the products, next to their use: the scheduling barriers keep
-    // them where they are.
+    // One step, `it` with it % AHEAD = q.  The next one's rows go from registers to
+    // LDS in its first half, and in the second those of the step AHEAD after it
+    // start on their way; each product's operands are read while the products
+    // before it run, and once used its weights are replaced by those of the step
+    // AHEAD of this one.  `full`: all these steps exist and lie wholly inside K.
+    // With three buffers one barrier is enough, in the middle, where no wave waits
+    // for it long: what is written here was last read two steps ago.
+    // The order is the one written here, one memory access after each product or
+    // two: the compiler would move the loads next to their use, and a wave that
+    // issues several at once waits for the memory pipe while its matrix core idles.
     i32x4 fa[2][TM];
     int cur = 0;
-    auto step = [&](auto full, int it) {
+    constexpr int kHalf = kStage / 2;
+    auto step = [&](auto full, int q, int it) {
         constexpr bool kFull = decltype(full)::value != 0;
-        const int next = cur == 2 ? 0 : cur + 1;
-        if (kFull || it + 1 < it1) {
-            store_rows(next);
-#pragma unroll
-            for (int j = 0; j < TN; ++j) bp[j] += 2 * kFragment;
-        }
-        if (kFull || it + 2 < it1) load_rows(full, it + 2);
-        __builtin_amdgcn_sched_barrier(0);
+        const int next = cur == 2 ? 0 : cur + 1, qn = (q + 1) % AHEAD;
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) {
-            if (ks < 3 || kFull || it + 1 < it1) {
+            constexpr int kOther = TM + kHalf, kProducts = TM * TN;
 #pragma unroll
-                for (int i = 0; i < TM; ++i)
-                    fa[(ks + 1) & 1][i] = ks < 3 ? frag(cur, i, ks + 1) : frag(next, i, 0);
+            for (int m = 0; m < kProducts; ++m) {
+                const int i = m % TM, j = m / TM;
+                acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[q][ks][j], fa[ks & 1][i],
+                                                                   acc[i][j], 0, 0, 0);
+#pragma unroll
+                for (int o = m * kOther / kProducts; o < (m + 1) * kOther / kProducts; ++o) {
+                    if (o < TM) {
+                        if (ks < 3)
+                            fa[(ks + 1) & 1][o] = frag(cur, o, ks + 1);
+                        else if (kFull || it + 1 < steps)
+                            fa[0][o] = frag(next, o, 0);
+                    } else if (ks < 2) {
+                        if (kFull || it + 1 < steps) store_row(qn, ks * kHalf + o - TM, next);
+                    } else if (kFull || it + 1 + AHEAD < steps) {
+                        load_row(full, qn, (ks - 2) * kHalf + o - TM, it + 1 + AHEAD);
+                    }
+                }
+                if (i == TM - 1 && (kFull || it + AHEAD < steps)) load_weight(q, ks, j, it + AHEAD);
+                __builtin_amdgcn_sched_barrier(0);
             }
-            __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-            for (int i = 0; i < TM; ++i)
-#pragma unroll
-                for (int j = 0; j < TN; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[ks][j], fa[ks & 1][i],
-                                                                       acc[i][j], 0, 0, 0);
-            __builtin_amdgcn_sched_barrier(0);
-            if (kFull || it + 1 < it1) load_weights(ks);
             if (ks == 1) __syncthreads();
             __builtin_amdgcn_sched_barrier(0);
         }
@@ -372,74 +454,74 @@ __global__ __launch_bounds__(WM *WN * 64) void gn_int8_tiles(MatmulArgs a) {
     };
     typedef std::integral_constant<int, 0> Any;
     typedef std::integral_constant<int, 1> Full;
-    load_rows(Any{}, it0);
-    store_rows(0);
-    // rows before weights, as in a step: a wait for the former is none for the latter
-    if (it0 + 1 < it1) load_rows(Any{}, it0 + 1);
-    __builtin_amdgcn_sched_barrier(0);
+    // Before the first step: its rows in LDS, its weights and what the next ones need
+    // on its way, in the order of a step, so that a wait for one is none for those
+    // after it (nor may a load be left out on the way to the full steps).
+    auto begin = [&](auto full) {
+        constexpr bool kFull = decltype(full)::value != 0;
 #pragma unroll
-    for (int ks = 0; ks < 4; ++ks) load_weights(ks);
-    __syncthreads();
+        for (int i = 0; i < kStage; ++i) load_row(full, 0, i, 0);
 #pragma unroll
-    for (int i = 0; i < TM; ++i) fa[0][i] = frag(0, i, 0);
-    int it = it0;
-    for (; it + 3 < it1; ++it) step(Full{}, it);
-    for (; it < it1; ++it) step(Any{}, it);
-    if (a.split > 1) {
-        i32x4 *to = a.part + (int64_t{blockIdx.x} * (kThreads / 64) + wave) * (TM * TN * 4 * 64) + lane;
+        for (int i = 0; i < kStage; ++i) store_row(0, i, 0);
 #pragma unroll
-        for (int i = 0; i < TM; ++i)
+        for (int q = 0; q < AHEAD; ++q) {
 #pragma unroll
-            for (int j = 0; j < TN; ++j)
+            for (int ks = 0; ks < 4; ++ks) {
+                __builtin_amdgcn_sched_barrier(0);
+                if (ks >= 2 && (kFull || q + 1 < steps)) {
 #pragma unroll
-                for (int g = 0; g < 4; ++g)
-                    to[((i * TN + j) * 4 + g) * 64] =
-                        i32x4{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2],
-                              acc[i][j][4 * g + 3]};
-        return;
+                    for (int i = 0; i < kHalf; ++i)
+                        load_row(full, (q + 1) % AHEAD, (ks - 2) * kHalf + i, q + 1);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+                if (kFull || q < steps) {
+#pragma unroll
+                    for (int j = 0; j < TN; ++j) load_weight(q, ks, j, q);
+                }
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < TM; ++i) fa[0][i] = frag(0, i, 0);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    int it = 0;
+    if (it + 2 * AHEAD + 1 < steps) {
+        begin(Full{});
+        for (; it + 2 * AHEAD + 1 < steps; it += AHEAD) {
+#pragma unroll
+            for (int q = 0; q < AHEAD; ++q) step(Full{}, q, it + q);
+        }
+    } else {
+        begin(Any{});
     }
+    for (; it < steps; it += AHEAD) {
+#pragma unroll
+        for (int q = 0; q < AHEAD; ++q)
+            if (it + q < steps) step(Any{}, q, it + q);
+    }
+    float scale[TM];
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
-        const int64_t m = m0 + (wm * TM + i) * 32 + (lane & 31);
+        const int64_t m = m0 + i * 32 + (lane & 31);
+        scale[i] = a.sa[m < a.M ? m : a.M - 1];
+    }
 #pragma unroll
-        for (int j = 0; j < TN; ++j)
+    for (int j = 0; j < TN; ++j)
 #pragma unroll
-            for (int p = 0; p < 2; ++p) {
-                i32x4 g[2];
+        for (int p = 0; p < 2; ++p) {
+            i32x4 lo[TM], hi[TM];
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
+            for (int i = 0; i < TM; ++i) {
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) g[h][r] = acc[i][j][8 * p + 4 * h + r];
-                join_halves(g[0], g[1]);
-                finish8<D>(a, m, n0 + (wn * TN + j) * 32 + p * 16 + (lane >> 5) * 8, g[0], g[1]);
+                for (int r = 0; r < 4; ++r) {
+                    lo[i][r] = acc[i][j][8 * p + r];
+                    hi[i][r] = acc[i][j][8 * p + 4 + r];
+                }
+                join_halves(lo[i], hi[i]);
             }
-    }
-}
-
-// The parts of K joined: one wave's lanes as they hold a product's sums.
-template <class D, int WM, int WN, int TM, int TN>
-__global__ __launch_bounds__(256) void gn_int8_join(MatmulArgs a) {
-    constexpr int kWaves = WM * WN, kEach = TM * TN * 2;  // pairs of groups in a wave
-    const int lane = threadIdx.x & 63;
-    const int tiles = a.mt * a.nt;
-    const int64_t u = int64_t{blockIdx.x} * 4 + (threadIdx.x >> 6);
-    if (u >= int64_t{tiles} * kWaves * kEach) return;
-    const int b = static_cast<int>(u / (kWaves * kEach)), in = static_cast<int>(u % (kWaves * kEach));
-    const int wave = in / kEach, pair = in % kEach;
-    const i32x4 *from = a.part + u * 128 + lane;
-    const int64_t next = int64_t{tiles} * kWaves * kEach * 128;
-    i32x4 g0 = {}, g1 = {};
-    for (int s = 0; s < a.split; ++s) {
-        g0 += from[s * next];
-        g1 += from[s * next + 64];
-    }
-    join_halves(g0, g1);
-    int tm, tn;
-    tile_of(b, tiles, a.mt, a.nt, &tm, &tn);
-    const int i = pair / 2 / TN, j = pair / 2 % TN;
-    finish8<D>(a, int64_t{tm} * (32 * TM * WM) + (wave / WN * TM + i) * 32 + (lane & 31),
-               tn * (32 * TN * WN) + (wave % WN * TN + j) * 32 + pair % 2 * 16 + (lane >> 5) * 8, g0,
-               g1);
+            finish8<D, TM>(a, m0 + (lane & 31), n0 + j * 32 + p * 16 + (lane >> 5) * 8, scale, lo, hi);
+        }
 }
 
 // ---- host -----------------------------------------------------------------------
@@ -470,27 +552,50 @@ gn_status check_nk(int64_t N, int64_t K) {
     return GN_OK;
 }
 
+constexpr int64_t kMaxTiles = int64_t{1} << 23;  // a dispatch holds fewer than 2^32 work-items
+
 // Which kernel takes a product, and in what tiles.
 struct MatmulPlan {
-    int kind;  // 0: few rows; 1: tiles of 128 x 128; 2: of 256 x 256
-    int mt, nt, split;
-    size_t workspace;
+    int bm, bn;   // rows and channels of a tile
+    bool rows;    // gn_int8_rows, else gn_int8_tiles
+    int mt, nt;
 };
 
-MatmulPlan matmul_plan(int64_t M, int64_t N, int64_t K) {
-    MatmulPlan p{};
-    p.split = 1;
-    if (M <= 64) return p;
-    const int64_t big = ceil_div(M, 256) * ceil_div(N, 256);
-    p.kind = big >= 192 ? 2 : 1;
-    const int64_t side = p.kind == 2 ? 256 : 128;
-    p.mt = static_cast<int>(ceil_div(M, side));
-    p.nt = static_cast<int>(ceil_div(N, side));
-    const int64_t tiles = int64_t{p.mt} * p.nt, steps = k_blocks(K) / 2;
-    if (p.kind == 1)
-        while (tiles * p.split * 2 <= 512 && steps / (p.split * 2) >= 4) p.split *= 2;
-    if (p.split > 1) p.workspace = static_cast<size_t>(tiles * p.split * side * side * 4);
-    return p;
+// The kernel and tile with the least estimated time: the tiles that the busiest of
+// the 256 CUs gets, times what one costs, which is proportional to K.  `cost` is in
+// tenths of a microsecond at K = 4096.  A tile of the rows kernel is bound by its
+// CU's traffic with the L2 and costs its rows and channels, about 1 us for 16 of
+// them; the tiles kernel's were measured.  Measured, us for 1 / 2 / 4 / 8 tiles a
+// CU (bf16, K = 4096): rows 16x16 5.8 / 7 / 9.1 / 15, 32x32 7.4 / 9.4 / 16 / 29,
+// 32x64 8.2 / 14 / 26 / 47, 64x64 11.3 / 20 / 36 / 69; tiles 64x128 15.6 / 25 / 45 /
+// 84, 128x128 23.7 / 40 / 76, 128x256 38 / 67 / 125 / 245.  kStart: a tiles launch
+// takes 2 us longer to start and end, whatever K is.
+MatmulPlan matmul_plan(int64_t M, int64_t N, int64_t K, int64_t a_stride) {
+    struct Kind {
+        int bm, bn;
+        bool rows;
+        int64_t cost;
+    };
+    static constexpr Kind kinds[] = {
+        {16, 16, true, 20},   {16, 32, true, 30},     {16, 64, true, 50},
+        {32, 16, true, 30},   {32, 32, true, 40},     {32, 64, true, 60},
+        {48, 32, true, 50},   {48, 64, true, 70},     {64, 32, true, 60},
+        {64, 64, true, 80},   {64, 128, false, 98},   {128, 128, false, 174},
+        {128, 256, false, 295},
+    };
+    constexpr int64_t kCus = 256, kStart = 20 * 4096;
+    // the tiles kernel keeps 32-bit distances from a tile's first row
+    const bool near = a_stride < int64_t{1} << 24;
+    const Kind *best = nullptr;
+    int64_t least = 0;
+    for (const Kind &k : kinds) {
+        if (!k.rows && !near) continue;
+        const int64_t tiles = ceil_div(M, k.bm) * ceil_div(N, k.bn);
+        const int64_t cost = ceil_div(tiles, kCus) * k.cost * K + (k.rows ? 0 : kStart);
+        if (best == nullptr || cost < least) best = &k, least = cost;
+    }
+    return MatmulPlan{best->bm, best->bn, best->rows, static_cast<int>(ceil_div(M, best->bm)),
+                      static_cast<int>(ceil_div(N, best->bn))};
 }
 
 }  // namespace
@@ -526,20 +631,26 @@ gn_status gn_int8_pack_weights(const void *codes, int64_t codes_stride, void *pa
     return finish_launch();
 }
 
-gn_status gn_int8_matmul_workspace(int64_t M, int64_t N, int64_t K, int64_t *bytes_out) {
-    if (bytes_out == nullptr || M < 0) return GN_INVALID_ARGUMENT;
+gn_status gn_int8_matmul_plan(int64_t M, int64_t N, int64_t K, int64_t a_stride,
+                              int64_t plan_out[4]) {
+    if (plan_out == nullptr || M < 0 || a_stride < 0) return GN_INVALID_ARGUMENT;
     const gn_status st = check_nk(N, K);
     if (st != GN_OK) return st;
     if (M > GN_INT8_MAX_M) return GN_UNSUPPORTED;
-    *bytes_out = static_cast<int64_t>(matmul_plan(M, N, K).workspace);
+    const MatmulPlan p = matmul_plan(M, N, K, a_stride);
+    const int64_t tiles = int64_t{p.mt} * p.nt;
+    if (tiles >= kMaxTiles) return GN_UNSUPPORTED;
+    plan_out[0] = p.bm;
+    plan_out[1] = p.bn;
+    plan_out[2] = p.rows ? 0 : 1;
+    plan_out[3] = tiles;
     return GN_OK;
 }
 
 gn_status gn_int8_matmul(const void *a, int64_t a_stride, const float *a_scales, const void *packed,
                          const float *w_scales, const void *bias, const void *residual,
                          int64_t residual_stride, void *z, int64_t z_stride, int64_t M, int64_t N,
-                         int64_t K, int dtype, void *workspace, int64_t workspace_bytes,
-                         void *stream) {
+                         int64_t K, int dtype, void *stream) {
     if (a == nullptr || a_scales == nullptr || packed == nullptr || w_scales == nullptr ||
         z == nullptr)
         return GN_INVALID_ARGUMENT;
@@ -555,19 +666,14 @@ gn_status gn_int8_matmul(const void *a, int64_t a_stride, const float *a_scales,
     if (M > GN_INT8_MAX_M) return GN_UNSUPPORTED;
     const int64_t es = elem_bytes(dtype);
     if (misaligned(a_scales, 4) || misaligned(w_scales, 4) || misaligned(packed, 16) ||
-        misaligned(residual, es) || misaligned(z, es) || misaligned(workspace, 16))
+        misaligned(residual, es) || misaligned(z, es))
         return GN_UNSUPPORTED;
     if (M == 0) return GN_OK;
-    const MatmulPlan plan = matmul_plan(M, N, K);
-    const size_t need = plan.workspace;
-    if (need > 0 && workspace == nullptr) return GN_INVALID_ARGUMENT;
-    if (need > 0 && (workspace_bytes < 0 || static_cast<size_t>(workspace_bytes) < need))
-        return GN_SCRATCH_TOO_SMALL;
+    const MatmulPlan plan = matmul_plan(M, N, K, a_stride);
+    const int64_t tiles = int64_t{plan.mt} * plan.nt;
+    if (tiles >= kMaxTiles) return GN_UNSUPPORTED;
     Call c;
-    st = begin_call(stream,
-                    {a, a_scales, packed, w_scales, bias, residual, z,
-                     need > 0 ? workspace : nullptr},
-                    &c);
+    st = begin_call(stream, {a, a_scales, packed, w_scales, bias, residual, z}, &c);
     if (st != GN_OK) return st;
     MatmulArgs p{};
     p.a = static_cast<const int8_t *>(a);
@@ -588,35 +694,35 @@ gn_status gn_int8_matmul(const void *a, int64_t a_stride, const float *a_scales,
     p.bias_type = affine_type(dtype);
     p.mt = plan.mt;
     p.nt = plan.nt;
-    p.split = plan.split;
-    p.part = static_cast<i32x4 *>(workspace);
+    const unsigned grid = static_cast<unsigned>(tiles);
     by_type(dtype, [&](auto d) {
         using D = decltype(d);
+        constexpr int kWaves = 8;
         auto rows = [&](auto mt, auto nt) {
-            constexpr int MT = decltype(mt)::value, NT = decltype(nt)::value, WAVES = 8;
-            const dim3 grid(static_cast<unsigned>(ceil_div(p.nb, NT)),
-                            static_cast<unsigned>(ceil_div(M, 16 * MT)));
-            gn_int8_rows<D, MT, NT, WAVES><<<grid, WAVES * 64, 0, c.stream>>>(p);
+            gn_int8_rows<D, decltype(mt)::value, decltype(nt)::value, kWaves>
+                <<<grid, kWaves * 64, 0, c.stream>>>(p);
         };
-        auto tiles = [&](auto wm, auto wn, auto tm, auto tn) {
-            constexpr int WM = decltype(wm)::value, WN = decltype(wn)::value;
-            constexpr int TM = decltype(tm)::value, TN = decltype(tn)::value;
-            const unsigned n = static_cast<unsigned>(p.mt) * static_cast<unsigned>(p.nt);
-            gn_int8_tiles<D, WM, WN, TM, TN>
-                <<<n * static_cast<unsigned>(p.split), WM * WN * 64, 0, c.stream>>>(p);
-            if (p.split > 1)
-                gn_int8_join<D, WM, WN, TM, TN>
-                    <<<static_cast<unsigned>(ceil_div(int64_t{n} * WM * WN * TM * TN * 2, 4)), 256,
-                       0, c.stream>>>(p);
+        auto by_n = [&](auto mt) {
+            switch (plan.bn) {
+                case 16: return rows(mt, IC<1>{});
+                case 32: return rows(mt, IC<2>{});
+                default: return rows(mt, IC<4>{});
+            }
         };
-        if (plan.kind == 2)
-            tiles(IC<2>{}, IC<4>{}, IC<4>{}, IC<2>{});
-        else if (plan.kind == 1)
-            tiles(IC<2>{}, IC<2>{}, IC<2>{}, IC<2>{});
-        else if (M <= 16)
-            rows(IC<1>{}, IC<1>{});
+        if (plan.rows) {
+            switch (plan.bm) {
+                case 16: return by_n(IC<1>{});
+                case 32: return by_n(IC<2>{});
+                case 48: return by_n(IC<3>{});
+                default: return by_n(IC<4>{});
+            }
+        }
+        if (plan.bm == 64)
+            gn_int8_tiles<D, 4, 2, 1, 2><<<grid, 256, 0, c.stream>>>(p);
+        else if (plan.bn == 128)
+            gn_int8_tiles<D, 4, 4, 1, 2><<<grid, 256, 0, c.stream>>>(p);
         else
-            rows(IC<4>{}, IC<2>{});
+            gn_int8_tiles<D, 4, 4, 2, 1><<<grid, 256, 0, c.stream>>>(p);
     });
     return finish_launch();
 }

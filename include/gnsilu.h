@@ -509,20 +509,25 @@ gn_status gn_rms_norm_rows_backward(const void *dy, int64_t dy_stride, const voi
  * The sums are int32 and exact; scales, bias and residual are applied in fp32
  * and z is rounded once.  Codes may be any int8 value.  z == residual with the
  * same stride is allowed.  Supported: K <= GN_INT8_MAX_K, N <= GN_INT8_MAX_N,
- * M <= GN_INT8_MAX_M, else GN_UNSUPPORTED; packed 16-byte aligned, workspace
- * too. */
+ * M <= GN_INT8_MAX_M, else GN_UNSUPPORTED; packed 16-byte aligned.  No
+ * workspace: nothing is shared between calls. */
 #define GN_INT8_MAX_K 65536
 #define GN_INT8_MAX_N (1 << 20)
 #define GN_INT8_MAX_M (1 << 20)
 gn_status gn_int8_packed_bytes(int64_t N, int64_t K, int64_t *bytes_out);
 gn_status gn_int8_pack_weights(const void *codes, int64_t codes_stride, void *packed, int64_t N,
                                int64_t K, void *stream);
-gn_status gn_int8_matmul_workspace(int64_t M, int64_t N, int64_t K, int64_t *bytes_out);
 gn_status gn_int8_matmul(const void *a, int64_t a_stride, const float *a_scales, const void *packed,
                          const float *w_scales, const void *bias, const void *residual,
                          int64_t residual_stride, void *z, int64_t z_stride, int64_t M, int64_t N,
-                         int64_t K, int dtype, void *workspace, int64_t workspace_bytes,
-                         void *stream);
+                         int64_t K, int dtype, void *stream);
+
+/* Launch shape of gn_int8_matmul for a problem, for inspection and tests; no HIP
+ * call.  Writes 4 values: [0] rows and [1] channels of a tile, [2] 0 when the
+ * waves of a workgroup share out K (few rows), 1 when they share out the tile's
+ * channels, [3] workgroups launched. */
+gn_status gn_int8_matmul_plan(int64_t M, int64_t N, int64_t K, int64_t a_stride,
+                              int64_t plan_out[4]);
 
 /* The GroupNorm(+SiLU) fused into the neighbouring 3x3 convolution of the
  * decoder's ResnetBlock2D (Modifications section 2: "ResnetBlock2D

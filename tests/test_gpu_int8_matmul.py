@@ -73,6 +73,38 @@ def test_sizes(gn, M, N, K, dtype):
         check(z, x, w, bias if with_b else None, res if with_r else None, dtype, what)
 
 
+# (rows, channels) of a tile, kernel; sizes that take it, ragged in both, at one and
+# more steps of 128 input channels
+KINDS = [
+    (16, 16, 0, [(148, 1, 65), (5, 100, 1500)]), (16, 32, 0, [(3, 4499, 65), (2, 7001, 1300)]),
+    (16, 64, 0, [(13, 10283, 67)]), (32, 16, 0, [(2124, 33, 72)]),
+    (32, 32, 0, [(20, 4161, 69), (27, 4161, 1200)]), (32, 64, 0, [(56, 4124, 66), (59, 4133, 1100)]),
+    (48, 32, 0, [(33, 5529, 71)]), (48, 64, 0, [(66, 5719, 67), (90, 5719, 513)]),
+    (64, 32, 0, [(2800, 135, 71)]), (64, 64, 0, [(99, 6028, 65), (250, 4090, 600)]),
+    (64, 128, 1, [(4378, 5520, 115), (1698, 7005, 228), (1163, 6533, 380), (718, 6808, 504),
+                  (706, 6901, 550), (643, 5387, 736), (513, 6796, 867), (522, 6709, 922)]),
+    (128, 128, 1, [(4482, 4174, 128), (1928, 5286, 230), (4672, 1548, 347), (4637, 1569, 403),
+                   (4130, 713, 618), (4898, 589, 741), (390, 7010, 773), (387, 7026, 969)]),
+    (128, 256, 1, [(3867, 3995, 123), (1090, 6390, 256), (842, 7012, 319), (4948, 1164, 454),
+                   (4907, 1189, 613), (4882, 1168, 715), (4471, 1315, 845), (4875, 1186, 979)]),
+]
+
+
+@pytest.mark.parametrize("bm,bn,kernel,size,i", [(m, n, k, s, i) for m, n, k, sizes in KINDS
+                                                 for i, s in enumerate(sizes)])
+def test_every_tile(gn, bm, bn, kernel, size, i):
+    M, N, K = size
+    plan = gn.int8_matmul_plan(M, N, K)
+    assert (plan["rows"], plan["channels"], plan["tiles_kernel"]) == (bm, bn, kernel)
+    dtype = DTYPES[(i + bm // 16) % 3]
+    print("case int8_matmul tile %s %s" % (size, dtype), flush=True)
+    x, w = make(gn, M, N, K, dtype, M + K, (0, -K % 16, 3)[i % 3])
+    bias, res = extras(M, N, dtype, (torch.float32, dtype)[i % 2], N)
+    res = None if i % 4 == 3 else res
+    z = gn.int8_matmul(x, gn.pack_int8_weight(w), bias, residual=res)
+    check(z, x, w, bias, res, dtype, size)
+
+
 @pytest.mark.parametrize("M", [1, 3, 16, 17, 40, 64, 65, 128, 200, 300])
 def test_bits_do_not_depend_on_the_rows_beside(gn, M):
     """A row's result is the same in any batch: its sums are exact."""

@@ -48,9 +48,8 @@ def pack(codes=P[0], cs=64, packed=P[1], N=32, K=64):
 
 
 def product(a=P[0], as_=64, sa=P[1], w=P[2], sw=P[3], bias=P[4], res=P[5], rs=32, z=P[6], zs=32,
-            M=4, N=32, K=64, dtype=0, ws=P[7], size=1 << 40):
-    return gn.gn_int8_matmul(a, as_, sa, w, sw, bias, res, rs, z, zs, M, N, K, dtype, ws, size,
-                             None)
+            M=4, N=32, K=64, dtype=0):
+    return gn.gn_int8_matmul(a, as_, sa, w, sw, bias, res, rs, z, zs, M, N, K, dtype, None)
 
 
 @pytest.mark.parametrize("fn,kw", [
@@ -78,7 +77,7 @@ def product(a=P[0], as_=64, sa=P[1], w=P[2], sw=P[3], bias=P[4], res=P[5], rs=32
     (product, dict(sw=None)), (product, dict(z=None)), (product, dict(M=-1)),
     (product, dict(N=0)), (product, dict(K=-1)), (product, dict(dtype=3)),
     (product, dict(zs=31)), (product, dict(as_=-16)), (product, dict(rs=-1)),
-    (product, dict(as_=BIG)), (product, dict(M=300, K=16384, as_=16384, ws=None)),
+    (product, dict(as_=BIG)),
 ])
 def test_invalid(fn, kw):
     assert fn(**kw) == GnStatus.INVALID_ARGUMENT
@@ -95,7 +94,7 @@ def test_invalid(fn, kw):
     (quantize, dict(scales=TWO)),
     (widen, dict(C=16385, xs=16385)), (widen, dict(x=ODD)), (widen, dict(scales=TWO)),
     (pack, dict(packed=EIGHT)), (pack, dict(K=65537)), (pack, dict(N=(1 << 20) + 1)),
-    (product, dict(w=EIGHT)), (product, dict(ws=EIGHT)), (product, dict(sa=TWO)),
+    (product, dict(w=EIGHT)), (product, dict(sa=TWO)),
     (product, dict(sw=TWO)), (product, dict(bias=TWO)), (product, dict(bias=ODD, dtype=0x20)),
     (product, dict(res=ODD)), (product, dict(z=ODD)), (product, dict(K=65537, as_=65552)),
     (product, dict(N=(1 << 20) + 1, zs=1 << 21)), (product, dict(M=(1 << 20) + 1)),
@@ -138,18 +137,23 @@ def test_workspace_sizes():
     assert size_of(pb, 4, 65537)[0] == GnStatus.UNSUPPORTED
     assert pb(4, 4, None) == GnStatus.INVALID_ARGUMENT
 
-    mw = gn.gn_int8_matmul_workspace
-    for M in (1, 16, 64):               # few rows need none
-        assert size_of(mw, M, 4096, 4096) == (GnStatus.OK, 0)
-    st, n = size_of(mw, 300, 32, 16384)     # few tiles: K in parts
-    assert st == GnStatus.OK and n >= 2 * 4 * 300 * 32
-    assert product(M=300, K=16384, as_=16384, size=n - 1) == GnStatus.SCRATCH_TOO_SMALL
-    assert product(M=300, K=16384, as_=16384, size=-1) == GnStatus.SCRATCH_TOO_SMALL
-    assert size_of(mw, -1, 32, 64)[0] == GnStatus.INVALID_ARGUMENT
-    assert size_of(mw, 1, 0, 64)[0] == GnStatus.INVALID_ARGUMENT
-    assert size_of(mw, 1, 32, 65537)[0] == GnStatus.UNSUPPORTED
-    assert size_of(mw, (1 << 20) + 1, 32, 64)[0] == GnStatus.UNSUPPORTED
-    assert mw(1, 32, 64, None) == GnStatus.INVALID_ARGUMENT
+
+def test_product_plan():
+    plan = gn.int8_matmul_plan
+    for M, N, K in ((1, 1, 1), (1, 4096, 4096), (300, 500, 700), (1 << 20, 17, 65536),
+                    (4096, 1 << 20, 1)):
+        p = plan(M, N, K)
+        assert p["workgroups"] == -(-M // p["rows"]) * -(-N // p["channels"]) < 1 << 23
+    assert plan(1, 4096, 4096) == dict(rows=16, channels=16, tiles_kernel=0, workgroups=256)
+    assert plan(16384, 4096, 4096)["tiles_kernel"] == 1
+    # rows too far apart for 32-bit distances within a tile
+    assert plan(16384, 4096, 4096, 1 << 24)["tiles_kernel"] == 0
+    assert plan(1 << 20, 1 << 20, 64) is None       # more workgroups than a launch holds
+    fn, out = gn.gn_int8_matmul_plan, (ctypes.c_int64 * 4)()
+    assert fn(1, 1, 1, 1, None) == GnStatus.INVALID_ARGUMENT
+    assert fn(-1, 1, 1, 1, out) == fn(1, 0, 1, 1, out) == GnStatus.INVALID_ARGUMENT
+    assert fn(1, 1, 1, -1, out) == GnStatus.INVALID_ARGUMENT
+    assert fn(1, 1, 65537, 1, out) == GnStatus.UNSUPPORTED
 
 
 # ---- the binding ---------------------------------------------------------------
