@@ -123,6 +123,14 @@ __device__ __forceinline__ void finish4(const MatmulArgs &a, int64_t m, int n, c
     }
 }
 
+// Between one wave's accesses to LDS that its other lanes made or will make: LDS
+// works in order, the compiler is told to.
+__device__ __forceinline__ void wave_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // The tile of a workgroup: consecutive workgroups go to the eight XCDs in turn,
 // each of which takes a run of tiles, in strips of kStrip rows of tiles, so
 // that the tiles it works on at one time share rows and weights in its L2.
@@ -214,10 +222,7 @@ __global__ __launch_bounds__(WAVES * 64) void gn_int8_rows(MatmulArgs a) {
         const bool more = it + WAVES < steps;
 #pragma unroll
         for (int i = 0; i < 2 * MT; ++i) own[i * 64 + lane] = sa[i];
-        // the lanes of one wave: LDS works in order, the compiler is told to
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+        wave_sync();
         if (more) load_rows(it + WAVES);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -237,9 +242,7 @@ __global__ __launch_bounds__(WAVES * 64) void gn_int8_rows(MatmulArgs a) {
             if (more) load_weights(it + WAVES, u);
             __builtin_amdgcn_sched_barrier(0);
         }
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+        wave_sync();
     }
 #pragma unroll
     for (int i = 0; i < MT; ++i)
@@ -256,17 +259,42 @@ __global__ __launch_bounds__(WAVES * 64) void gn_int8_rows(MatmulArgs a) {
 }
 
 // ---- tiles -----------------------------------------------------------------------
-// Scales and bias of eight neighbouring channels; those behind N count nothing.
-struct Channels8 {
-    float s[8], b[8];
-    __device__ __forceinline__ Channels8(const MatmulArgs &a, int n) {
-        if (n + 8 <= a.N) {
-            load_affine<8>(a.sb, Affine::kF32, n, 1.0f, s);
-            load_affine<8>(a.bias, a.bias_type, n, 0.0f, b);
-            return;
-        }
+// The end of a wave's TM x TN products of 32 x 32.  Each leaves four neighbouring
+// channels of 32 rows in an instruction's lanes, 8 bytes of z: turned in the wave's
+// own part of LDS, 32 rows at a time, lanes next to each other hold a row's
+// neighbouring 16 bytes of z instead, so that residual and z move in runs of 64 to
+// 256 bytes.  All of the residual is on its way before the first row is turned.
+template <class D, int TM, int TN, class Acc>
+__device__ __forceinline__ void finish_tile(const MatmulArgs &a, int64_t m0, int n0, const Acc &acc,
+                                            i32x4 *own, int lane) {
+    using T = typename D::storage;
+    constexpr int W = 16 / sizeof(T), kLanes = 32 * TN / W;  // lanes of a row
+    constexpr int kRows = 64 / kLanes, kTimes = 32 / kRows;  // rows at a time, times for 32
+    constexpr int kPitch = 8 * TN + 1;                       // pieces of 4 sums from row to row
+    const int n = n0 + lane % kLanes * W, r0 = lane / kLanes;
+    const bool whole = n + W <= a.N;
+    T *z = static_cast<T *>(a.z) + n;
+    const T *res = static_cast<const T *>(a.res) + n;
+    // (half of it for fp32, for the registers)
+    constexpr int kAhead = sizeof(T) == 2 ? TM : TM / 2;
+    Piece<D, W> pr[kAhead][kTimes];
+    auto load_residual = [&](int i) {
+        if (a.res == nullptr || !whole) return;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int t = 0; t < kTimes; ++t) {
+            const int64_t m = m0 + i * 32 + t * kRows + r0;
+            if (m < a.M) pr[i % kAhead][t].template load<false>(res + m * a.res_stride);
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) load_residual(i);
+    float s[W], b[W];
+    if (whole) {
+        load_affine<W>(a.sb, Affine::kF32, n, 1.0f, s);
+        load_affine<W>(a.bias, a.bias_type, n, 0.0f, b);
+    } else {
+#pragma unroll
+        for (int j = 0; j < W; ++j) {  // channels behind N count nothing
             const int c = n + j < a.N ? n + j : a.N - 1;
             float v[1];
             load_affine<1>(a.bias, a.bias_type, c, 0.0f, v);
@@ -274,67 +302,48 @@ struct Channels8 {
             b[j] = v[0];
         }
     }
-};
-
-// Eight neighbouring sums of TM rows (32 apart) from channel n on, scaled and
-// stored; the residual's loads all before the first store.
-template <class D, int TM>
-__device__ __forceinline__ void finish8(const MatmulArgs &a, int64_t m0, int n, const float (&sa)[TM],
-                                        const i32x4 (&lo)[TM], const i32x4 (&hi)[TM]) {
-    using T = typename D::storage;
-    if (n >= a.N) return;
-    const Channels8 ch(a, n);
-    T *z = static_cast<T *>(a.z) + m0 * a.z_stride + n;
-    const T *res = static_cast<const T *>(a.res) + m0 * a.res_stride + n;
-    constexpr int W = sizeof(T) == 2 ? 8 : 4;
-    const bool whole = n + 8 <= a.N;
-    Piece<D, W> r[TM][8 / W];
-    if (a.res != nullptr && whole) {
-#pragma unroll
-        for (int i = 0; i < TM; ++i)
-#pragma unroll
-            for (int k = 0; k < 8 / W; ++k)
-                if (m0 + i * 32 < a.M)
-                    r[i][k].template load<false>(res + i * 32 * a.res_stride + k * W);
-    }
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
-        if (m0 + i * 32 >= a.M) break;
-        float o[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            o[j] = fmaf(static_cast<float>(j < 4 ? lo[i][j & 3] : hi[i][j & 3]) * sa[i], ch.s[j],
-                        ch.b[j]);
-        if (whole) {
+        for (int j = 0; j < TN; ++j)
 #pragma unroll
-            for (int k = 0; k < 8 / W; ++k) {
-                float v[W];
+            for (int g = 0; g < 4; ++g)
+                own[(lane & 31) * kPitch + j * 8 + g * 2 + (lane >> 5)] =
+                    i32x4{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2],
+                          acc[i][j][4 * g + 3]};
+        wave_sync();
+        i32x4 v[kTimes][W / 4];
 #pragma unroll
-                for (int j = 0; j < W; ++j)
-                    v[j] = a.res != nullptr ? o[k * W + j] + r[i][k].get(j) : o[k * W + j];
-                Piece<D, W>::template store<false>(z + i * 32 * a.z_stride + k * W, v);
-            }
-        } else {
+        for (int t = 0; t < kTimes; ++t)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                if (n + j >= a.N) break;
-                if (a.res != nullptr) o[j] += D::to_f32(res[i * 32 * a.res_stride + j]);
-                z[i * 32 * a.z_stride + j] = D::from_f32(o[j]);
+            for (int k = 0; k < W / 4; ++k)
+                v[t][k] = own[(t * kRows + r0) * kPitch + lane % kLanes * (W / 4) + k];
+        wave_sync();
+#pragma unroll
+        for (int t = 0; t < kTimes; ++t) {
+            const int64_t m = m0 + i * 32 + t * kRows + r0;
+            if (m >= a.M || n >= a.N) continue;
+            const float sa = a.sa[m];
+            float o[W];
+#pragma unroll
+            for (int j = 0; j < W; ++j)
+                o[j] = fmaf(static_cast<float>(v[t][j / 4][j % 4]) * sa, s[j], b[j]);
+            if (whole) {
+                if (a.res != nullptr) {
+#pragma unroll
+                    for (int j = 0; j < W; ++j) o[j] += pr[i % kAhead][t].get(j);
+                }
+                Piece<D, W>::template store<false>(z + m * a.z_stride, o);
+            } else {
+#pragma unroll
+                for (int j = 0; j < W; ++j) {
+                    if (n + j >= a.N) break;
+                    if (a.res != nullptr) o[j] += D::to_f32(res[m * a.res_stride + j]);
+                    z[m * a.z_stride + j] = D::from_f32(o[j]);
+                }
             }
         }
-    }
-}
-
-// A 32 x 32 product leaves 4 neighbouring sums of channels 8g + 4*(lane / 32) in
-// each lane, of row lane % 32.  Swapped between the halves of the wave, two g's
-// become 8 neighbours: channels 16*pair + 8*(lane / 32) and up.
-__device__ __forceinline__ void join_halves(i32x4 &g0, i32x4 &g1) {
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        const auto s = __builtin_amdgcn_permlane32_swap(static_cast<uint32_t>(g0[r]),
-                                                        static_cast<uint32_t>(g1[r]), false, false);
-        g0[r] = static_cast<int>(s[0]);
-        g1[r] = static_cast<int>(s[1]);
+        if (i + kAhead < TM) load_residual(i + kAhead);
     }
 }
 
@@ -500,28 +509,10 @@ __global__ __launch_bounds__(WN * 64, 2) void gn_int8_tiles(MatmulArgs a) {
         for (int q = 0; q < AHEAD; ++q)
             if (it + q < steps) step(Any{}, q, it + q);
     }
-    float scale[TM];
-#pragma unroll
-    for (int i = 0; i < TM; ++i) {
-        const int64_t m = m0 + i * 32 + (lane & 31);
-        scale[i] = a.sa[m < a.M ? m : a.M - 1];
-    }
-#pragma unroll
-    for (int j = 0; j < TN; ++j)
-#pragma unroll
-        for (int p = 0; p < 2; ++p) {
-            i32x4 lo[TM], hi[TM];
-#pragma unroll
-            for (int i = 0; i < TM; ++i) {
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    lo[i][r] = acc[i][j][8 * p + r];
-                    hi[i][r] = acc[i][j][8 * p + 4 + r];
-                }
-                join_halves(lo[i], hi[i]);
-            }
-            finish8<D, TM>(a, m0 + (lane & 31), n0 + j * 32 + p * 16 + (lane >> 5) * 8, scale, lo, hi);
-        }
+    __syncthreads();  // rows' buffers are free
+    constexpr int kOwn = 3 * BM * 8 / WN;
+    static_assert(kOwn >= 32 * (8 * TN + 1), "32 rows of a wave's sums");
+    finish_tile<D, TM, TN>(a, m0, n0, acc, &rows[0][0] + wave * kOwn, lane);
 }
 
 // ---- host -----------------------------------------------------------------------
