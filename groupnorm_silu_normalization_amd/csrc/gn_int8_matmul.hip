@@ -49,25 +49,28 @@ struct MatmulArgs {
 constexpr int kKBlock = 64, kNBlock = 16, kFragment = 1024;
 
 // ---- packing ---------------------------------------------------------------------
-// One lane, 16 bytes of a fragment.
+// A lane makes 16 bytes of a fragment at a time; the grid goes through all of them
+// (up to 2^32, more than a dispatch holds lanes).
+constexpr int64_t kPackBlocks = 1 << 16;
 __global__ __launch_bounds__(256) void gn_int8_pack(const int8_t *w, int64_t stride, int8_t *packed,
                                                     int N, int K, int kb, int64_t pieces) {
-    const int64_t i = int64_t{blockIdx.x} * 256 + threadIdx.x;
-    if (i >= pieces) return;
-    const int lane = static_cast<int>(i & 63);
-    const int64_t f = i >> 6;
-    const int64_t n = f / kb * kNBlock + (lane & 15);
-    const int64_t k = f % kb * kKBlock + (lane >> 4) * 16;
-    uint32_t v[4] = {0, 0, 0, 0};
-    if (n < N) {
+    for (int64_t i = int64_t{blockIdx.x} * 256 + threadIdx.x; i < pieces;
+         i += int64_t{gridDim.x} * 256) {
+        const int lane = static_cast<int>(i & 63);
+        const int64_t f = i >> 6;
+        const int64_t n = f / kb * kNBlock + (lane & 15);
+        const int64_t k = f % kb * kKBlock + (lane >> 4) * 16;
+        uint32_t v[4] = {0, 0, 0, 0};
+        if (n < N) {
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-            if (k + j < K)
-                v[j >> 2] |= static_cast<uint32_t>(static_cast<uint8_t>(w[n * stride + k + j]))
-                             << (8 * (j & 3));
+            for (int j = 0; j < 16; ++j)
+                if (k + j < K)
+                    v[j >> 2] |= static_cast<uint32_t>(static_cast<uint8_t>(w[n * stride + k + j]))
+                                 << (8 * (j & 3));
+        }
+        u32x4 o = {v[0], v[1], v[2], v[3]};
+        reinterpret_cast<u32x4 *>(packed)[i] = o;
     }
-    u32x4 o = {v[0], v[1], v[2], v[3]};
-    reinterpret_cast<u32x4 *>(packed)[i] = o;
 }
 
 // ---- the end of a product ----------------------------------------------------------
@@ -616,7 +619,8 @@ gn_status gn_int8_pack_weights(const void *codes, int64_t codes_stride, void *pa
     st = begin_call(stream, {codes, packed}, &c);
     if (st != GN_OK) return st;
     const int64_t pieces = n_blocks(N) * k_blocks(K) * 64;
-    gn_int8_pack<<<static_cast<unsigned>(ceil_div(pieces, 256)), 256, 0, c.stream>>>(
+    gn_int8_pack<<<static_cast<unsigned>(std::min(ceil_div(pieces, 256), kPackBlocks)), 256, 0,
+                   c.stream>>>(
         static_cast<const int8_t *>(codes), codes_stride, static_cast<int8_t *>(packed),
         static_cast<int>(N), static_cast<int>(K), static_cast<int>(k_blocks(K)), pieces);
     return finish_launch();

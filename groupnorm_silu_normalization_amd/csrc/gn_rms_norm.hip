@@ -477,6 +477,7 @@ gn_status gn_rms_norm_rows(const void *x, int64_t x_stride, const void *residual
     if (x == nullptr || (y == nullptr) == (codes == nullptr)) return GN_INVALID_ARGUMENT;
     if ((codes == nullptr) != (scales == nullptr) || (residual == nullptr) != (h == nullptr))
         return GN_INVALID_ARGUMENT;
+    if (y != nullptr && y == h) return GN_INVALID_ARGUMENT;  // two outputs
     if (!(eps >= 0.0f) || std::isinf(eps)) return GN_INVALID_ARGUMENT;
     const int64_t in[2] = {x_stride, residual == nullptr ? 0 : residual_stride};
     const int64_t out[2] = {y == nullptr ? codes_stride : y_stride, h == nullptr ? C : h_stride};

@@ -257,3 +257,74 @@ def test_offsets_beyond_32_bits(gn):
     zbuf = torch.empty(2 * zs + N, device="cuda")
     z = zbuf.as_strided((3, N), (zs, 1))
     assert torch.equal(gn.int8_matmul(x, p, out=z), gn.int8_matmul(x, p))
+
+
+def test_one_row_without_a_batch(gn):
+    x, w = make(gn, 5, 40, 70, torch.bfloat16, 3)
+    p = gn.pack_int8_weight(w)
+    one = gn.Rows8(x.codes[2].contiguous(), x.scales[2].clone(), torch.bfloat16)
+    assert one.shape == (70,) and one.scales.shape == ()
+    z = gn.int8_matmul(one, p)
+    assert z.shape == (40,) and torch.equal(z, gn.int8_matmul(x, p)[2])
+    v = torch.randn(70, device="cuda").bfloat16()
+    q, h = gn.rms_norm_rows(v, residual=v, quantize=True)
+    assert q.shape == (70,) and h.shape == (70,) and q.scales.shape == ()
+    q2 = gn.rms_norm_rows(v[None], residual=v[None], quantize=True)[0]
+    assert torch.equal(q.codes, q2.codes[0]) and torch.equal(gn.quantize_rows(v).codes,
+                                                             gn.quantize_rows(v[None]).codes[0])
+    assert gn.dequantize_rows(q).shape == (70,)
+
+
+def test_streams_and_threads_at_once(gn):
+    """Calls of every kernel at once share nothing."""
+    import threading
+    cases = []
+    for M, N, K in ((1, 500, 700), (40, 5529, 300), (600, 700, 900), (1163, 6533, 380)):
+        x, w = make(gn, M, N, K, torch.bfloat16, M)
+        cases.append((x, gn.pack_int8_weight(w)))
+    want = [gn.int8_matmul(x, p) for x, p in cases]
+    torch.cuda.synchronize()
+    got, errors = {}, []
+
+    def work(t):
+        try:
+            with torch.no_grad(), torch.cuda.stream(torch.cuda.Stream()):
+                r = [[gn.int8_matmul(x, p) for x, p in cases] for _ in range(5)]
+                torch.cuda.current_stream().synchronize()
+                got[t] = r
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(t,)) for t in range(3)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors and len(got) == 3
+    for r in got.values():
+        for zs in r:
+            for z, z0 in zip(zs, want):
+                assert torch.equal(z, z0)
+
+
+def test_two_captured_graphs_replayed_beside_eager_work(gn):
+    x, w = make(gn, 700, 900, 500, torch.float16, 4)
+    y, _ = make(gn, 9, 900, 500, torch.float16, 5)
+    p = gn.pack_int8_weight(w)
+    gn.int8_matmul(x, p), gn.int8_matmul(y, p)
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for r in (x, y):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(gn.int8_matmul(r, p))
+        graphs.append(g)
+    for k in range(4):
+        for r in (x, y):
+            r.codes.random_(-128, 128, generator=torch.Generator(device="cuda").manual_seed(k))
+        graphs[k % 2].replay()
+        eager = [gn.int8_matmul(r, p) for r in (x, y)]
+        graphs[1 - k % 2].replay()
+        torch.cuda.synchronize()
+        for a, b in zip(outs, eager):
+            assert torch.equal(a, b)

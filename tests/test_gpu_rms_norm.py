@@ -311,6 +311,7 @@ def test_declined_and_refused_on_the_gpu(gn):
                  lambda: gn.rms_norm_rows(x, residual_out=x),
                  lambda: gn.rms_norm_rows(x, out=x[:2]),
                  lambda: gn.rms_norm_rows(x, eps=-1.0),
+                 lambda: gn.rms_norm_rows(x, residual=x, out=(y := x.clone()), residual_out=y),
                  lambda: gn.rms_norm_rows_backward(x, x, st[:3]),
                  lambda: gn.rms_norm_rows_backward(x, x[:2], st),
                  lambda: gn.rms_norm_rows_backward(x, x, st, residual_grad=x[:2])):

@@ -54,7 +54,7 @@ def product(a=P[0], as_=64, sa=P[1], w=P[2], sw=P[3], bias=P[4], res=P[5], rs=32
 
 @pytest.mark.parametrize("fn,kw", [
     (norm, dict(x=None)), (norm, dict(y=None)), (norm, dict(codes=P[6], scales=P[7])),
-    (norm, dict(res=None)), (norm, dict(h=None)), (norm8, dict(scales=None)),
+    (norm, dict(res=None)), (norm, dict(h=None)), (norm, dict(h=P[4])), (norm8, dict(scales=None)),
     (norm8, dict(codes=None)), (norm, dict(scales=P[7])), (norm, dict(eps=-1.0)),
     (norm, dict(eps=float("nan"))), (norm, dict(eps=float("inf"))), (norm, dict(dtype=3)),
     (norm, dict(dtype=0x40)), (norm, dict(xs=-1)), (norm, dict(rs=-1)), (norm, dict(hs=63)),
