@@ -55,13 +55,22 @@ __global__ __launch_bounds__(THREADS) void gn_quantize(Rows8Args a) {
     int par = 0;
     loop.run(fetch, [&](Row &r, int64_t m, bool live) {
         // channels counted twice (a last piece's, those of a lane beyond the
-        // row) change no maximum
+        // row) change no maximum; magnitudes of every type order like their bits
         uint32_t top = 0;
+        if constexpr (W == 8) {
+            uint32_t m = 0;
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
+            for (int j = 0; j < NV; ++j)
 #pragma unroll
-            for (int i = 0; i < W; ++i)
-                top = max(top, __float_as_uint(r.v[j].get(i)) & 0x7fffffffu);
+                for (int k = 0; k < 4; ++k) m = max2_u16(m, r.v[j].w[k] & 0x7fff7fffu);
+            top = max(m >> 16, m & 0xffffu);
+        } else {
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+#pragma unroll
+                for (int i = 0; i < W; ++i)
+                    top = max(top, __float_as_uint(r.v[j].get(i)) & 0x7fffffffu);
+        }
         top = lane_max<(TPR < 64 ? TPR : 64)>(top);
         if constexpr (TPR > 64) {
             constexpr int kWaves = TPR / 64;
@@ -72,6 +81,7 @@ __global__ __launch_bounds__(THREADS) void gn_quantize(Rows8Args a) {
             par ^= 1;
         }
         if (!live) return;  // no barrier from here on
+        if constexpr (W == 8) top = __float_as_uint(D::to_f32(static_cast<uint16_t>(top)));
         const Rows8Scale sc(top);
         if (t == 0) a.scales_out[m] = Rows8Scale::step(top);
 #pragma unroll

@@ -8,10 +8,11 @@
 // order of a sum.  A row that holds an infinity or a NaN has the scale NaN and
 // codes 0; a row of zeros has codes 0.
 //
-// The quotient is taken as t * (127 / top) in fp32, off by less than 2^-15 (two
-// roundings of at most 127): only a value that close to a border between two
-// codes may get the wrong one.  Those (one value in 2^14) are settled in fp64,
-// where 127 * t - q * top and top / 2 are exact: 31 bits of products.
+// The quotient is taken as t * (127 * (1 / top)) with v_rcp_f32 (one unit in the
+// last place), one rounding and a fused product: off by less than 127 * 1.5 * 2^-23,
+// which is less than 2^-15, so only a value that close to a border between two codes
+// may get the wrong one.  Those (one value in 2^14) are settled in fp64, where
+// 127 * t - q * top and top / 2 are exact: 31 bits of products.
 #pragma once
 
 #include "gn_rows.hpp"
@@ -28,7 +29,7 @@ struct Rows8Scale {
         const bool none = top_bits == 0u || top_bits >= 0x7f800000u;
         top = none ? 1.0f : __uint_as_float(top_bits);
         up = top < 0x1p-100f ? 0x1p100f : 1.0f;
-        inv = 127.0f / (top * up);
+        inv = 127.0f * __builtin_amdgcn_rcpf(top * up);
         keep = none ? 0u : ~0u;
     }
     // top / 127; NaN, 0 or the quotient
@@ -53,13 +54,18 @@ __device__ __forceinline__ float rows8_settle(float t, float top, float q) {
 template <int W>
 __device__ __forceinline__ Codes<W> rows8_encode(const float (&t)[W], const Rows8Scale &s) {
     uint32_t b[W];
-    float far = 0.0f;
+    float far = 0.0f, v[W];
+#pragma unroll
+    for (int j = 0; j < W; ++j) v[j] = t[j];
+    if (s.up != 1.0f) {
+#pragma unroll
+        for (int j = 0; j < W; ++j) v[j] *= s.up;
+    }
 #pragma unroll
     for (int j = 0; j < W; ++j) {
-        const float f = (t[j] * s.up) * s.inv;
-        const float r = f + 12582912.0f;
+        const float r = fmaf(v[j], s.inv, 12582912.0f);
         b[j] = __float_as_uint(r);
-        far = fmaxf(far, fabsf(f - (r - 12582912.0f)));
+        far = fmaxf(far, fabsf(fmaf(v[j], s.inv, 12582912.0f - r)));
     }
     if (far > 0.5f - 0x1p-15f) {
 #pragma unroll
