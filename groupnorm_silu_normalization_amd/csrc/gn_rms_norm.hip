@@ -10,11 +10,10 @@
 //              dx = rstd*(g - n*sum(g*n)/C) + dh, dgamma[c] = sum over rows of dy*n
 //
 // As layer norm the passes are bound by HBM: a row is read once, held in
-// registers and written once, the next row's loads in flight meanwhile.  One sum
-// is enough (no mean is taken off, so nothing cancels), and in 8 bits the row's
-// maximum goes through the same exchange as its sum: rstd is a factor of the
-// whole row and drops out of the codes, so that both are taken of values that
-// are known before any sum.
+// registers and written once.  One sum is enough (no mean is taken off, so
+// nothing cancels), and in 8 bits the row's maximum goes through the same exchange
+// as its sum: rstd is a factor of the whole row and drops out of the codes, so
+// that both are taken of values that are known before any sum.
 //
 // dh is the gradient that reaches h past the norm, through the residual stream:
 // added here it costs one read, where a kernel of its own would read both and
@@ -105,7 +104,7 @@ __global__ __launch_bounds__(THREADS) void gn_rms_norm(RmsArgs a) {
             if constexpr (RES) r.r[j].template load<false>(res + m * a.res_stride + c[j]);
         }
     };
-    RowLoop<Row, kSlots, sizeof(T) == 2 || NV < 4> loop{a.M, slot, gridDim.x};
+    RowLoop<Row, kSlots, sizeof(T) == 4 && NV < 4> loop{a.M, slot, gridDim.x};
     loop.begin(fetch);
     float ga[NV][W];
 #pragma unroll
@@ -400,7 +399,12 @@ __global__ __launch_bounds__(THREADS) void gn_rms_norm_backward(RmsArgs a) {
 template <class D>
 void launch_rms_forward(const LnShape &s, const RmsArgs &a, hipStream_t st) {
     const int nt = forward_threads(s.tpr);
-    const int64_t blocks = std::min(ceil_div(a.M, nt / s.tpr), kForwardLanes / nt);
+    constexpr int64_t kBytes = sizeof(typename D::storage);
+    int64_t blocks = one_each_blocks(a.M, nt / s.tpr);
+    if (kBytes == 4)  // with a row ahead
+        blocks = std::min(blocks, kForwardLanes / nt);
+    else if (a.codes_out == nullptr && a.M <= kOneEachBytes / (a.C * kBytes))
+        blocks = std::min(blocks, 2 * kForwardLanes / nt);
     with_ln_shape<D, true>(s, [&](auto w, auto tail, auto tpr, auto nv) {
         constexpr int W = decltype(w)::value, TPR = decltype(tpr)::value;
         constexpr int NV = decltype(nv)::value, NT = forward_threads(TPR);

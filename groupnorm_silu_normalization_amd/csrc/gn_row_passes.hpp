@@ -251,6 +251,18 @@ void with_ln_shape(const LnShape &s, F &&f) {
 constexpr int forward_threads(int tpr) { return tpr < 256 ? 256 : tpr; }
 constexpr int backward_threads(int tpr, int nv) { return nv == 1 || tpr > 512 ? 1024 : 512; }
 
+// Workgroups of a forward pass without loads ahead, whose slots take a row each:
+// other rows' waves hide a row's latency, and those that hold one row at a time are
+// more.  Measured, us with a row ahead and kForwardLanes / with a row a slot (bf16):
+// quantize (16384,4096) 42.0 / 38.3, (8192,2560) 19.4 / 17.3; norm with residual
+// into 8 bits 93.0 / 86.9, 36.1 / 32.3, into bf16 104.0 / 96.0, 30.0 / 31.6, the
+// last 29.3 with two rows a slot, which share gamma's loads (where x is in the
+// caches: up to 64 MiB of it).
+constexpr int64_t kOneEachBytes = int64_t{64} << 20;
+inline int64_t one_each_blocks(int64_t M, int slots) {
+    return std::min(ceil_div(M, slots), int64_t{1} << 21);
+}
+
 inline int64_t backward_blocks(const LnShape &s, int64_t M) {
     const int64_t slots = backward_threads(s.tpr, s.nv) / s.tpr;
     return std::max(std::min(ceil_div(M, slots), kBackwardBlocks), ceil_div(M, slots * kMaxRun));

@@ -6,7 +6,7 @@
 //
 // Both are bound by HBM.  A row is read once and held in registers while its
 // lanes agree on the maximum, in the lanes and pieces of the norms' forward
-// passes (gn_row_passes.hpp), the next row's loads in flight meanwhile.
+// passes (gn_row_passes.hpp).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -50,7 +50,7 @@ __global__ __launch_bounds__(THREADS) void gn_quantize(Rows8Args a) {
 #pragma unroll
         for (int j = 0; j < NV; ++j) r.v[j].template load<false>(x + m * a.x_stride + c[j]);
     };
-    RowLoop<Row, kSlots, sizeof(T) == 2 || NV < 4> loop{a.M, slot, gridDim.x};
+    RowLoop<Row, kSlots, sizeof(T) == 4 && NV < 4> loop{a.M, slot, gridDim.x};
     loop.begin(fetch);
     int par = 0;
     loop.run(fetch, [&](Row &r, int64_t m, bool live) {
@@ -115,7 +115,7 @@ __global__ __launch_bounds__(THREADS) void gn_dequantize(Rows8Args a) {
         for (int j = 0; j < NV; ++j) r.q[j].load(a.codes + m * a.codes_stride + c[j]);
         r.scale = a.scales[m];
     };
-    RowLoop<Row, kSlots, true> loop{a.M, slot, gridDim.x};
+    RowLoop<Row, kSlots, sizeof(T) == 4> loop{a.M, slot, gridDim.x};
     loop.begin(fetch);
     loop.run(fetch, [&](Row &r, int64_t m, bool live) {
         if (!live) return;
@@ -135,8 +135,10 @@ template <class F> void launch_rows(int64_t M, int64_t C, int dtype, F &&go) {
     by_type(dtype, [&](auto d) {
         with_ln_shape<decltype(d), true>(s, [&](auto w, auto tail, auto tpr, auto nv) {
             constexpr int TPR = decltype(tpr)::value, NT = forward_threads(TPR);
-            go(d, w, tail, tpr, nv, IC<NT>{},
-               static_cast<unsigned>(std::min(ceil_div(M, NT / TPR), kForwardLanes / NT)), s.P);
+            int64_t blocks = one_each_blocks(M, NT / TPR);
+            if (sizeof(typename decltype(d)::storage) == 4)  // with a row ahead
+                blocks = std::min(blocks, kForwardLanes / NT);
+            go(d, w, tail, tpr, nv, IC<NT>{}, static_cast<unsigned>(blocks), s.P);
         });
     });
 }

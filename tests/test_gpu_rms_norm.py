@@ -109,6 +109,22 @@ def test_many_rows(gn, M, C, dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("M,C", [(5000, 2560), (17001, 513), (1500, 9000)])
+def test_several_rows_a_slot(gn, M, C, dtype):
+    """Forward passes of more rows than the launches' row slots."""
+    what = (M, C, dtype)
+    print("case rms_norm slots %s" % (what,), flush=True)
+    x, r, w, _ = make(M, C, dtype, dtype, M + C)
+    check_forward(gn, x, r, w, EPS, what)
+    check_forward(gn, x, None, w, EPS, what)
+    q = gn.quantize_rows(x.cuda())
+    check_codes(q, *ref.quantize(x), what)
+    want = q.codes.cpu().double() * q.scales.cpu().double().unsqueeze(-1)
+    rows.check(gn.dequantize_rows(q), want, rows.U * want.abs() + rows.rounded(want, dtype),
+               "%s widened" % (what,))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("C", [1, 3, 8, 15, 33, 65, 257, 513, 1001, 1030, 2049, 2560, 4097, 8193,
                                16383])
 def test_gradient_from_a_checkpoint(gn, C, dtype):
