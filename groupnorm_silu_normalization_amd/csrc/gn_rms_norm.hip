@@ -18,6 +18,12 @@
 // dh is the gradient that reaches h past the norm, through the residual stream:
 // added here it costs one read, where a kernel of its own would read both and
 // write again.
+//
+// Measured on MI355X: (16384,4096) bf16 with a residual 93 us (5.8 TB/s), backward
+// with dh 95 us (5.65 TB/s) and column sums 4.9; (4099,1003) fp16 with a residual
+// into 8 bits 9.6 us; backward (5001,1537) from the checkpoint 14.7 us and 3.9 (its
+// start and end and five rows a slot; three rows ahead instead of one took 10%
+// longer).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

@@ -7,6 +7,10 @@
 // Both are bound by HBM.  A row is read once and held in registers while its
 // lanes agree on the maximum, in the lanes and pieces of the norms' forward
 // passes (gn_row_passes.hpp).
+//
+// Measured on MI355X, bf16: quantize (16384,4096) 38 us (5.3 TB/s), (8192,2560)
+// 12.7 us (5.0 TB/s, the VALU 95% busy: 320 pieces on 512 places); dequantize 33 us
+// (6.1 TB/s), 10.6 us.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

@@ -503,7 +503,8 @@ gn_status gn_rms_norm_rows_backward(const void *dy, int64_t dy_stride, const voi
  * and for each output channel:
  *     z[m][n] = (sum_k a[m][k]*w[n][k]) * a_scales[m] * w_scales[n]
  *               + bias[n] + residual[m][n]
- * a: int8, row m at m * a_stride (any alignment); packed: the weights w [N][K] as
+ * a: int8, row m at m * a_stride (any alignment; up to 15 bytes behind a row, but
+ * none behind the last, may be read and count nothing); packed: the weights w [N][K] as
  * gn_int8_pack_weights lays them out, w_scales [N]; bias: N values of the
  * GN_AFFINE_* type of dtype, or null; residual and z: dtype, or residual null.
  * The sums are int32 and exact; scales, bias and residual are applied in fp32
