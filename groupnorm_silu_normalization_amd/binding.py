@@ -1072,6 +1072,14 @@ class PackedInt8Weight:
     (gn_int8_pack_weights), with its scales, for repeated products."""
 
     def __init__(self, data, scales, N, K):
+        torch = _torch()
+        if data.dtype != torch.int8 or scales.dtype != torch.float32:
+            raise TypeError("a packed weight holds int8 data and fp32 scales")
+        if (data.numel() != _workspace_bytes("gn_int8_packed_bytes", N, K)
+                or scales.shape != (N,) or not (data.is_contiguous() and scales.is_contiguous())):
+            raise ValueError("data and scales must be those of a packed (%d, %d) weight" % (N, K))
+        if data.device != scales.device:
+            raise ValueError("data and scales must be on one device")
         self.data, self.scales, self.shape = data, scales, (N, K)
         self.device = data.device
 

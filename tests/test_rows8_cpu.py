@@ -209,6 +209,20 @@ def test_rows8_object():
         gn.Rows8(codes, torch.zeros(6)[::2], torch.float16)
 
 
+def test_packed_weight_object():
+    size = size_of(gn.gn_int8_packed_bytes, 20, 70)[1]
+    data, scales = torch.zeros(size, dtype=torch.int8), torch.zeros(20)
+    assert gn.PackedInt8Weight(data, scales, 20, 70).shape == (20, 70)
+    for bad in ((data.float(), scales), (data, scales.double())):
+        with pytest.raises(TypeError):
+            gn.PackedInt8Weight(*bad, 20, 70)
+    for bad in ((data[:-1], scales, 20, 70), (data, scales[:19], 20, 70), (data, scales, 20, 700),
+                (data, scales, 33, 70), (data, torch.zeros(40)[::2], 20, 70),
+                (data, scales, 0, 70)):
+        with pytest.raises(ValueError):
+            gn.PackedInt8Weight(*bad)
+
+
 def test_reference_codes_are_nearest_and_ties_even():
     g = torch.Generator().manual_seed(3)
     t = torch.randn(50, 200, generator=g)
