@@ -140,7 +140,8 @@ __device__ __forceinline__ void wave_sync() {
 
 // The tile of a workgroup: consecutive workgroups go to the eight XCDs in turn,
 // each of which takes a run of tiles, in strips of kStrip rows of tiles, so
-// that the tiles it works on at one time share rows and weights in its L2.
+// that the tiles it works on at one time share rows and weights in its L2 (strips
+// of 8 or 16 take the same time within 2%: the products' power bounds large ones).
 constexpr int kStrip = 4;
 __device__ __forceinline__ void tile_of(int b, int tiles, int mt, int nt, int *tm, int *tn) {
     const int xcd = b & 7, per = tiles >> 3, rest = tiles & 7;
