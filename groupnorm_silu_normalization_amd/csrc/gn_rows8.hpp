@@ -19,8 +19,10 @@
 
 namespace gnsilu {
 
-// What a row's values are multiplied by: 127 / top, with values and `top` scaled
-// up first where the quotient would leave fp32's range.
+// What a row's values are multiplied by: 127 / top, with values and `top` brought
+// nearer to one first where 1 / top would not be a normal number (v_rcp_f32 gives 0
+// for top > 2^126) or 127 / top would leave fp32's range.  By powers of two: only
+// values below 2^-26 of a row above 2^100 round, far below half a code.
 struct Rows8Scale {
     float top, inv, up;
     uint32_t keep;  // mask of the codes' bytes: 0 for a row without values
@@ -28,7 +30,7 @@ struct Rows8Scale {
     __device__ __forceinline__ explicit Rows8Scale(uint32_t top_bits) {
         const bool none = top_bits == 0u || top_bits >= 0x7f800000u;
         top = none ? 1.0f : __uint_as_float(top_bits);
-        up = top < 0x1p-100f ? 0x1p100f : 1.0f;
+        up = top < 0x1p-100f ? 0x1p100f : top > 0x1p100f ? 0x1p-100f : 1.0f;
         inv = 127.0f * __builtin_amdgcn_rcpf(top * up);
         keep = none ? 0u : ~0u;
     }

@@ -462,7 +462,8 @@ gn_status gn_silu_rows_backward(const void *dy, const void *x, const void *codes
  * is left as it was), any alignment; scales: fp32 [M]. */
 gn_status gn_quantize_rows(const void *x, int64_t x_stride, void *codes, int64_t codes_stride,
                            float *scales, int64_t M, int64_t C, int dtype, void *stream);
-/* q * scale, rounded once to dtype. */
+/* q * scale, rounded once to dtype.  (127 * scale of fp32's largest number, whose
+ * 127th part is rounded up, rounds to infinity in fp32.) */
 gn_status gn_dequantize_rows(const void *codes, int64_t codes_stride, const float *scales, void *x,
                              int64_t x_stride, int64_t M, int64_t C, int dtype, void *stream);
 

@@ -1,0 +1,77 @@
+"""Rows in 8 bits, the root-mean-square norm and the product of 8-bit rows near the
+ends of the ranges that their definitions promise."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import rows8_reference as ref  # noqa: E402
+import rows_reference as rows  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+WIDE = [torch.bfloat16, torch.float32]      # the types with fp32's exponents
+
+
+@pytest.fixture(scope="module")
+def gn():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import groupnorm_silu_normalization_amd as gn
+    return gn
+
+
+@pytest.fixture(autouse=True)
+def no_grad():
+    with torch.no_grad():
+        yield
+
+
+def check_codes(q, codes, scales, es, what):
+    assert torch.equal(q.codes.cpu().to(torch.int64), codes), "%s codes" % (what,)
+    rows.check(q.scales, scales, es, "%s scales" % (what,))
+
+
+def border_rows(C, dtype):
+    """Values on the borders between two codes and one step of the type beside
+    them, in both signs, their largest magnitude 127 * 2^k for every k that the
+    type holds, and rows up to the type's largest number."""
+    k = torch.arange(C) % 127
+    t = (k + 0.5) * torch.where(torch.arange(C) % 2 == 0, 1.0, -1.0)
+    t[0] = 127.0
+    out = []
+    for e in (-100, -101, -106, -107, -108, 93, 94, 95, 100, 118, 119, 120, 121):
+        out.append((t.double() * 2.0 ** e).to(dtype))
+        near = out[-1].float() * (1 + torch.finfo(dtype).eps * (torch.arange(C) % 3 - 1))
+        near[0] = out[-1][0].float()
+        out.append(near.to(dtype))
+    top = torch.finfo(dtype).max
+    g = torch.Generator().manual_seed(C)
+    for largest in (top, top * 0.75, 2.0 ** 126, 2.0 ** 126 * (1 + 2.0 ** -7), 2.0 ** 127):
+        r = (torch.rand(C, generator=g) * 2 - 1).double() * largest
+        r[C // 2] = -largest
+        out.append(r.to(dtype))
+    return torch.stack(out)
+
+
+@pytest.mark.parametrize("dtype", WIDE)
+@pytest.mark.parametrize("C", [1, 3, 8, 127, 1280, 4097, 16384])
+def test_codes_over_the_types_range(gn, C, dtype):
+    x = border_rows(C, dtype)
+    q = gn.quantize_rows(x.cuda())
+    check_codes(q, *ref.quantize(x), "quantize %d %s" % (C, dtype))
+
+
+@pytest.mark.parametrize("dtype", WIDE)
+@pytest.mark.parametrize("C", [8, 127, 1280, 4097])
+def test_norm_codes_of_large_products(gn, C, dtype):
+    """Rows within the norm's range whose products with the weight go up to fp32's
+    largest numbers."""
+    t = border_rows(C, torch.float32)[-5:]
+    w = torch.full((C,), 2.0 ** 100)
+    w[1::3] = 2.0 ** 99
+    # at most 2^128 / 2^100, and (h * w) finite
+    h = (t.double() * 2.0 ** -100).to(dtype)
+    h = torch.where((h.double() * w.double()).abs() < torch.finfo(torch.float32).max, h, h * 0.5)
+    q = gn.rms_norm_rows(h.cuda(), w.cuda(), 1e-6, quantize=True)
+    _, _, _, wq, ws, _, _, es = ref.rms_norm(h, w, 1e-6, dtype)
+    check_codes(q, wq, ws, es, "rms_norm %d %s" % (C, dtype))
