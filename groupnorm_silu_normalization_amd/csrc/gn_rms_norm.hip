@@ -13,7 +13,10 @@
 // registers and written once.  One sum is enough (no mean is taken off, so
 // nothing cancels), and in 8 bits the row's maximum goes through the same exchange
 // as its sum: rstd is a factor of the whole row and drops out of the codes, so
-// that both are taken of values that are known before any sum.
+// that both are taken of values that are known before any sum.  The sum of squares
+// goes over the lanes times 2^-6: 16384 squares of 1e18 then stay below fp32's
+// largest number (2^127.6) and one square of 1e-18 above its smallest normal one
+// (2^-125.6).  A lane's own are at most 16.
 //
 // dh is the gradient that reaches h past the norm, through the residual stream:
 // added here it costs one read, where a kernel of its own would read both and
@@ -78,6 +81,9 @@ __device__ __forceinline__ void row_sum_max(float &s, uint32_t &top, float *red)
     }
 }
 
+// What a lane's sum of squares is multiplied by on its way to the row's; exact.
+constexpr float kSquares = 0x1p-6f;
+
 // ---------------------------------------------------------------------------
 // Forward.  RES: with a residual; CODES: y in 8 bits.
 // ---------------------------------------------------------------------------
@@ -115,7 +121,7 @@ __global__ __launch_bounds__(THREADS) void gn_rms_norm(RmsArgs a) {
     float ga[NV][W];
 #pragma unroll
     for (int j = 0; j < NV; ++j) load_affine<W>(a.af.gamma, a.af.type, c[j], 1.0f, ga[j]);
-    const float fc = static_cast<float>(a.C);
+    const float fc = static_cast<float>(a.C) * kSquares;
     int par = 0;
     loop.run(fetch, [&](Row &r, int64_t m, bool live) {
         float s = 0.0f;
@@ -135,6 +141,7 @@ __global__ __launch_bounds__(THREADS) void gn_rms_norm(RmsArgs a) {
                     top = max(top, __float_as_uint(r.v[j].get(i) * ga[j][i]) & 0x7fffffffu);
             }
         }
+        s *= kSquares;
         row_sum_max<TPR, CODES>(s, top, red + par * kRed);
         par ^= 1;
         if (!live) return;  // no barrier from here on

@@ -75,3 +75,31 @@ def test_norm_codes_of_large_products(gn, C, dtype):
     q = gn.rms_norm_rows(h.cuda(), w.cuda(), 1e-6, quantize=True)
     _, _, _, wq, ws, _, _, es = ref.rms_norm(h, w, 1e-6, dtype)
     check_codes(q, wq, ws, es, "rms_norm %d %s" % (C, dtype))
+
+
+@pytest.mark.parametrize("dtype", WIDE)
+@pytest.mark.parametrize("C", [1, 2, 8, 100, 341, 1024, 4096, 5000, 16384])
+def test_norm_at_the_ends_of_its_range(gn, C, dtype):
+    """Magnitudes just below 1e18, and just above 1e-18 without an eps: every
+    output of both passes."""
+    g = torch.Generator().manual_seed(C)
+    for M in (7, 1100):     # backward from columns read again, and from partial rows
+        sign = torch.where(torch.rand(M, C, generator=g) < 0.5, -1.0, 1.0)
+        size = 0.1 + 0.9 * torch.rand(M, C, generator=g)
+        size[0] = size[-1] = 1.0
+        w = 1 + 0.3 * torch.randn(C, generator=g)
+        dy = torch.randn(M, C, generator=g).to(dtype)
+        for x, eps in ((sign * size * 9.9e17, 1e-6), (sign * (1.02e-18 / size), 0.0)):
+            x = x.to(dtype)
+            xg, wg = x.cuda(), w.cuda()
+            what = "(%d, %d) %s eps %g" % (M, C, dtype, eps)
+            _, wy, wr, wq, ws, ey, er, es = ref.rms_norm(x, w, eps, dtype)
+            y, rstd = gn.rms_norm_rows(xg, wg, eps, stats=True)
+            rows.check(rstd, wr, er, what + " rstd")
+            rows.check(y, wy, ey, what + " y")
+            check_codes(gn.rms_norm_rows(xg, wg, eps, quantize=True), wq, ws, es, what)
+            dx, dw = gn.rms_norm_rows_backward(dy.cuda(), xg, rstd, wg)
+            wx, ww, ex, ew = ref.rms_norm_backward(dy, x, rstd, w, None, dtype, torch.float32,
+                                                   M + 16)
+            rows.check(dx, wx, ex, what + " dx")
+            rows.check(dw, ww, ew, what + " dw")
