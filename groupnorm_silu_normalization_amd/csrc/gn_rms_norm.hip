@@ -149,7 +149,7 @@ __global__ __launch_bounds__(THREADS) void gn_rms_norm(RmsArgs a) {
         if (t == 0 && a.rstd != nullptr) a.rstd[m] = rstd;
         if constexpr (CODES) {
             const Rows8Scale sc(top);
-            if (t == 0) a.scales_out[m] = Rows8Scale::step(top) * rstd;
+            if (t == 0) a.scales_out[m] = Rows8Scale::step(top, rstd);
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
                 if (lo[j] >= W) continue;

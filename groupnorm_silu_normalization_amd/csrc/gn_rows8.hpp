@@ -39,6 +39,12 @@ struct Rows8Scale {
         const float s = __uint_as_float(top_bits) / 127.0f;
         return top_bits >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : s;
     }
+    // top / 127 * rstd, where top / 127 alone may be subnormal
+    __device__ __forceinline__ static float step(uint32_t top_bits, float rstd) {
+        const bool small = top_bits < 0x0d800000u;  // 2^-100
+        const float s = step(__float_as_uint(__uint_as_float(top_bits) * (small ? 0x1p100f : 1.0f)));
+        return s * rstd * (small ? 0x1p-100f : 1.0f);
+    }
 };
 
 // A value next to a border between two codes: its code among q and q's neighbours.

@@ -103,3 +103,16 @@ def test_norm_at_the_ends_of_its_range(gn, C, dtype):
                                                    M + 16)
             rows.check(dx, wx, ex, what + " dx")
             rows.check(dw, ww, ew, what + " dw")
+
+
+@pytest.mark.parametrize("dtype", WIDE)
+def test_norm_scales_of_small_products(gn, dtype):
+    """A row's scale is that of its norm however small its products with the
+    weight are: their largest over 127 may be a subnormal number."""
+    C = 1000
+    g = torch.Generator().manual_seed(5)
+    h = (torch.randn(40, C, generator=g) * 1e-16).to(dtype)
+    w = torch.full((C,), 4e-23)
+    q = gn.rms_norm_rows(h.cuda(), w.cuda(), 0.0, quantize=True)
+    _, _, _, wq, ws, _, _, es = ref.rms_norm(h, w, 0.0, dtype)
+    check_codes(q, wq, ws, es, "small products %s" % dtype)
