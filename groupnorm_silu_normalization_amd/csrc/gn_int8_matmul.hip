@@ -100,6 +100,24 @@ template <class D> __device__ __forceinline__ void load4(const typename D::stora
     }
 }
 
+// W sums times their scales, plus b.  A sum is at most 2^30, so that times a row's
+// scale below 2^97 it is in fp32's range; with a larger one, which the channel's
+// scale may bring back, all is taken 2^-32-fold until the end (in fp64 instead, the
+// widest tiles spilt 60 registers).
+template <int W, class Sums>
+__device__ __forceinline__ void scaled(const Sums &acc, float sa, const float (&sb)[W],
+                                       const float (&b)[W], float (&o)[W]) {
+    if (fabsf(sa) >= 0x1p97f) {
+        sa *= 0x1p-32f;
+#pragma unroll
+        for (int j = 0; j < W; ++j)
+            o[j] = fmaf(static_cast<float>(acc(j)) * sa, sb[j], b[j] * 0x1p-32f) * 0x1p32f;
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < W; ++j) o[j] = fmaf(static_cast<float>(acc(j)) * sa, sb[j], b[j]);
+}
+
 // Four neighbouring sums of row m from channel n on, scaled and stored.
 template <class D>
 __device__ __forceinline__ void finish4(const MatmulArgs &a, int64_t m, int n, const i32x4 &acc) {
@@ -113,20 +131,21 @@ __device__ __forceinline__ void finish4(const MatmulArgs &a, int64_t m, int n, c
         load4<F32>(a.sb + n, sb);
         load_affine<4>(a.bias, a.bias_type, n, 0.0f, b);
         if (a.res != nullptr) load4<D>(res, r);
+        scaled<4>([&](int j) { return acc[j]; }, sa, sb, b, o);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            o[j] = fmaf(static_cast<float>(acc[j]) * sa, sb[j], b[j]) + r[j];
+        for (int j = 0; j < 4; ++j) o[j] += r[j];
         store4<D>(z, o);
         return;
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         if (n + j >= a.N) break;
-        float b[1];
+        float b[1], o[1];
+        const float sb[1] = {a.sb[n + j]};
         load_affine<1>(a.bias, a.bias_type, n + j, 0.0f, b);
-        float o = fmaf(static_cast<float>(acc[j]) * sa, a.sb[n + j], b[0]);
-        if (a.res != nullptr) o += D::to_f32(res[j]);
-        z[j] = D::from_f32(o);
+        scaled<1>([&](int) { return acc[j]; }, sa, sb, b, o);
+        if (a.res != nullptr) o[0] += D::to_f32(res[j]);
+        z[j] = D::from_f32(o[0]);
     }
 }
 
@@ -333,9 +352,7 @@ __device__ __forceinline__ void finish_tile(const MatmulArgs &a, int64_t m0, int
             if (m >= a.M || n >= a.N) continue;
             const float sa = a.sa[m];
             float o[W];
-#pragma unroll
-            for (int j = 0; j < W; ++j)
-                o[j] = fmaf(static_cast<float>(v[t][j / 4][j % 4]) * sa, s[j], b[j]);
+            scaled<W>([&](int j) { return v[t][j / 4][j % 4]; }, sa, s, b, o);
             if (whole) {
                 if (a.res != nullptr) {
 #pragma unroll

@@ -509,10 +509,12 @@ gn_status gn_rms_norm_rows_backward(const void *dy, int64_t dy_stride, const voi
  * gn_int8_pack_weights lays them out, w_scales [N]; bias: N values of the
  * GN_AFFINE_* type of dtype, or null; residual and z: dtype, or residual null.
  * The sums are int32 and exact; scales, bias and residual are applied in fp32
- * and z is rounded once.  Codes may be any int8 value.  z == residual with the
- * same stride is allowed.  Supported: K <= GN_INT8_MAX_K, N <= GN_INT8_MAX_N,
- * M <= GN_INT8_MAX_M, else GN_UNSUPPORTED; packed 16-byte aligned.  No
- * workspace: nothing is shared between calls. */
+ * and z is rounded once; whatever the sizes of the two scales, only a product of
+ * sum and both that leaves fp32's range gives an infinity.  Codes may be any int8
+ * value.  z == residual with the same stride is allowed.  Supported:
+ * K <= GN_INT8_MAX_K, N <= GN_INT8_MAX_N, M <= GN_INT8_MAX_M, else
+ * GN_UNSUPPORTED; packed 16-byte aligned.  No workspace: nothing is shared
+ * between calls. */
 #define GN_INT8_MAX_K 65536
 #define GN_INT8_MAX_N (1 << 20)
 #define GN_INT8_MAX_M (1 << 20)

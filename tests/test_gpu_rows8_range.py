@@ -116,3 +116,41 @@ def test_norm_scales_of_small_products(gn, dtype):
     q = gn.rms_norm_rows(h.cuda(), w.cuda(), 0.0, quantize=True)
     _, _, _, wq, ws, _, _, es = ref.rms_norm(h, w, 0.0, dtype)
     check_codes(q, wq, ws, es, "small products %s" % dtype)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("M,N,K,tiles", [(3, 70, 100, 0), (27, 4161, 1200, 0), (643, 5387, 736, 1),
+                                         (390, 7010, 773, 1), (842, 7012, 319, 1)])
+def test_product_of_rows_with_large_scales(gn, M, N, K, tiles, dtype):
+    """Rows whose sum times their own scale leaves fp32's range, which the
+    channel's scale brings back, beside ordinary rows."""
+    assert gn.int8_matmul_plan(M, N, K)["tiles_kernel"] == tiles
+    gen = torch.Generator().manual_seed(M)
+    a = torch.randint(-127, 128, (M, K), generator=gen, dtype=torch.int8)
+    a[1] = 0
+    b = torch.randint(-127, 128, (N, K), generator=gen, dtype=torch.int8)
+    sa = torch.tensor([2.6e36, 1e36, 1e33, 1.6e29, 1e29, 1e32])[torch.arange(M) % 6]
+    sb = (0.5 + torch.rand(N, generator=gen)) * (1e-38 if dtype == torch.float16 else 1e-33)
+    bias = torch.randn(N, generator=gen).to(dtype)
+    res = torch.randn(M, N, generator=gen).to(dtype)
+    x = gn.Rows8(a.cuda(), sa.cuda(), dtype)
+    p = gn.pack_int8_weight(gn.Rows8(b.cuda(), sb.cuda(), dtype))
+    for bi, r in ((None, None), (bias, res)):
+        z = gn.int8_matmul(x, p, None if bi is None else bi.cuda(),
+                           residual=None if r is None else r.cuda())
+        want, e = ref.matmul(a, sa, b, sb, bi, r, dtype)
+        # a product below fp32's normal numbers is rounded to them first
+        rows.check(z, want, e + 2.0 ** -149, "%s %s" % ((M, N, K), dtype))
+
+
+@pytest.mark.parametrize("M", [1, 300])
+@pytest.mark.parametrize("sa,sb", [(2.0 ** 97 * (1 - 2.0 ** -24), 2.0 ** -100), (2.0 ** 97, 2.0 ** -100),
+                                   (2.0 ** 121, 2.0 ** -140)])
+def test_largest_sums_with_large_scales(gn, M, sa, sb):
+    K, N = gn.INT8_MAX_K, 48
+    a = torch.full((M, K), -128, dtype=torch.int8, device="cuda")
+    x = gn.Rows8(a, torch.full((M,), sa, device="cuda"), torch.float32)
+    w = gn.Rows8(a[:1].expand(N, K).contiguous(), torch.full((N,), sb, device="cuda"),
+                 torch.float32)
+    z = gn.int8_matmul(x, gn.pack_int8_weight(w))
+    assert torch.equal(z.cpu().double(), torch.full((M, N), 2.0 ** 30 * sa * sb, dtype=torch.float64))
