@@ -1111,7 +1111,8 @@ def int8_matmul(x, weight, bias=None, *, residual=None, dtype=None, out=None):
 
     x: a Rows8 of shape (..., K) (``rms_norm_rows(quantize=True)``,
     ``quantize_rows``); weight: a PackedInt8Weight of shape (N, K), or a Rows8,
-    which is packed in the call; bias: N values in fp32, bf16 or fp16, or None;
+    which is packed in every call (31 us for 4096 x 4096, more than the product of
+    a thousand rows takes: keep the packed one); bias: N values in fp32, bf16 or fp16, or None;
     residual: (..., N) of z's type with evenly spaced rows, or None; ``out``
     may be residual.  None when the library declines the input."""
     if not isinstance(x, Rows8):

@@ -17,7 +17,8 @@
 // Measured on MI355X, bf16, us and TOP/s (a library product without scales in
 // brackets): (16384,4096,4096) 253, 2170 (244), (4096,4096,4096) 67 (66),
 // (1024,4096,4096) 24 (25), (256,4096,4096) 9.8 (10.8), (1001,1537,2003) 10.2,
-// (48,10240,2560) 6.4 (8.1), (1,4096,4096) 4.0 and 5.6 with weights from HBM.
+// (48,10240,2560) 6.4 to 7 (8.1), (1,4096,4096) 4.0, all with weights in the caches;
+// from HBM, a new copy of 640 MiB of them each time, the last two take 10.1 and 6.4.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -54,7 +55,8 @@ constexpr int kKBlock = 64, kNBlock = 16, kFragment = 1024;
 
 // ---- packing ---------------------------------------------------------------------
 // A lane makes 16 bytes of a fragment at a time; the grid goes through all of them
-// (up to 2^32, more than a dispatch holds lanes).
+// (up to 2^32, more than a dispatch holds lanes).  Its 16 loads of a byte bound it:
+// (4096,4096) takes 31 us, five times a copy, once for a weight's life.
 constexpr int64_t kPackBlocks = 1 << 16;
 __global__ __launch_bounds__(256) void gn_int8_pack(const int8_t *w, int64_t stride, int8_t *packed,
                                                     int N, int K, int kb, int64_t pieces) {
@@ -585,7 +587,10 @@ struct MatmulPlan {
 // CU (bf16, K = 4096): rows 16x16 5.8 / 7 / 9.1 / 15, 32x32 7.4 / 9.4 / 16 / 29,
 // 32x64 8.2 / 14 / 26 / 47, 64x64 11.3 / 20 / 36 / 69; tiles 64x128 15.6 / 25 / 45 /
 // 84, 128x128 23.7 / 40 / 76, 128x256 38 / 67 / 125 / 245.  kStart: a tiles launch
-// takes 2 us longer to start and end, whatever K is.
+// takes 2 us longer to start and end, whatever K is.  What a tile costs whatever K is
+// does not count, so that at K of one step many small tiles look cheaper than they
+// are: (16384,4096,16) takes 241 us in 16384 tiles of 64x64, (16384,4096,64) 41 us in
+// tiles of 128x256.
 MatmulPlan matmul_plan(int64_t M, int64_t N, int64_t K, int64_t a_stride) {
     struct Kind {
         int bm, bn;

@@ -256,8 +256,12 @@ constexpr int backward_threads(int tpr, int nv) { return nv == 1 || tpr > 512 ? 
 // more.  Measured, us with a row ahead and kForwardLanes / with a row a slot (bf16):
 // quantize (16384,4096) 42.0 / 38.3, (8192,2560) 19.4 / 17.3; norm with residual
 // into 8 bits 93.0 / 86.9, 36.1 / 32.3, into bf16 104.0 / 96.0, 30.0 / 31.6, the
-// last 29.3 with two rows a slot, which share gamma's loads (where x is in the
-// caches: up to 64 MiB of it).
+// last 29.3 with two rows a slot, which share gamma's loads (up to 64 MiB of x: the
+// two sizes measured hold 40 and 128).  fp32 rows keep kForwardLanes: up to 8192
+// channels they have a row ahead, and wider ones, which have no registers for it,
+// took with kForwardLanes / with a row a slot: norm (4096,9000) 50.1 / 58.5 us, into
+// 8 bits with residual 93.0 / 102.0, (2048,12288) 58.4 / 66.7, quantize (1500,9000)
+// 12.1 / 13.3, and at (16384,12288) the norm 291 / 284, quantize 187 / 171.
 constexpr int64_t kOneEachBytes = int64_t{64} << 20;
 inline int64_t one_each_blocks(int64_t M, int slots) {
     return std::min(ceil_div(M, slots), int64_t{1} << 21);
